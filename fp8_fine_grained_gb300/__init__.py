@@ -13,6 +13,12 @@ Entry points (same names as the C ABI):
     fp8_quant_128x128_dual(w)               -> (q, scales, qT, scalesT)
     fp8_gemm_blockscaled(mode, a, sa, b, sb, out_dtype) -> C
     fp8_grouped_gemm(xq, sx, row_index, expert_offsets, wq, sw, n_rows, out_dtype) -> Y
+    fp8_rmsnorm(x, gamma, eps, residual)    -> (q, scales, h, rstd)
+    fp8_rmsnorm_t(h, rstd, gamma)           -> (qT, scalesT)
+    fp8_rmsnorm_bwd(dy, h, rstd, gamma, dres) -> (dx, dgamma)
+    fp8_gated_gemm(xq, sx, wq, sw)          -> (h, scales, gu)
+    fp8_gated_bwd(gu, dh)                   -> (q, scales, qT, scalesT, hqT, hscalesT)
+    grad_clip(grads, max_norm)              -> (norm, out)
 plus the convenience wrappers fprop / dgrad / wgrad and device_status().
 """
 import ctypes
@@ -60,6 +66,17 @@ def lib():
         L.fp8_gemm_blockscaled_e4m3.argtypes = [I32, P, P, I64, I64, P, P, I64, I64, I64, I64, I64, P, I64, P, I64, P]
         L.fp8_grouped_gemm.argtypes = [P, P, I64, I64, P, P, ctypes.c_int32, I64, P, P, I64, I64, P, I32, I64, P]
         L.fp8_moe_combine.argtypes = [P, I64, I64, P, P, I64, I32, I64, P, I32, I64, P]
+        F32 = ctypes.c_float
+        L.fp8_rmsnorm.argtypes = [P, I64, P, I64, P, I32, I64, I64, F32, P, I64, P, I64, P, I64, P, I32, P]
+        L.fp8_rmsnorm_t.argtypes = [P, I64, P, P, I32, I64, I64, P, I64, P, I64, I32, P]
+        L.fp8_rmsnorm_bwd.argtypes = [P, I64, P, I64, P, P, I32, P, I64, I64, I64, P, I64, P, P, I64, P]
+        L.fp8_rmsnorm_bwd_workspace.argtypes = [I64, I64]
+        L.fp8_rmsnorm_bwd_workspace.restype = I64
+        L.fp8_gated_gemm.argtypes = [P, P, I64, I64, P, P, I64, I64, I64, I64, P, I64, P, I64, P, I64, I32, P]
+        L.fp8_gated_bwd.argtypes = [P, I64, P, I64, I64, I64, P, I64, P, I64, P, I64, P, I64, P, I64, P, I64, I32, P]
+        L.fp8fg_grad_clip.argtypes = [P, I64, F32, F32, P, P, I64, P]
+        L.fp8fg_grad_clip_workspace.argtypes = [I64]
+        L.fp8fg_grad_clip_workspace.restype = I64
         L.fp8fg_status_str.argtypes = [I32]
         L.fp8fg_status_str.restype = ctypes.c_char_p
         L.fp8fg_device_status.argtypes = [P]
@@ -563,6 +580,237 @@ def fp8_moe_combine(y, dest, w, out_dtype=None, out=None, stream=None):
                                _out_code(out.dtype), out.stride(0), _stream(stream))
     _check(rc, "fp8_moe_combine")
     return out
+
+
+# ------------------------------------------- between a gated MLP's GEMMs ----
+
+def _matrix(t, dtype, rows, cols, name):
+    """A 2-D row-major tensor of the dtype that covers [rows, cols]."""
+    _dtype(t, dtype, name)
+    _layout(t, name)
+    _at_least(t, rows, cols, name)
+
+
+def _vector(t, dtype, n, name):
+    _dtype(t, dtype, name)
+    if t.dim() != 1 or t.numel() < n or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous vector of at least %d entries" % (name, n))
+
+
+def _gamma_kind(gamma, D):
+    if gamma.dim() != 1 or gamma.numel() != D or not gamma.is_contiguous():
+        raise ValueError("gamma must be a contiguous vector of %d entries" % D)
+    return _out_code(gamma.dtype)
+
+
+def _workspace(nbytes, device, stream):
+    """Scratch of one call, allocated on the current stream; another stream
+    that uses it is recorded, so that the memory is not handed out while that
+    stream still runs."""
+    w = _torch().empty(nbytes, dtype=_torch().uint8, device=device)
+    if stream is not None and w.is_cuda:
+        w.record_stream(stream)
+    return w
+
+
+def fp8_rmsnorm(x, gamma, eps=1e-6, residual=None, h=None, q=None, scales=None, rstd=None, stream=None, pow2=False):
+    """Residual addition, RMS norm and 1x128 E4M3 quantisation.
+
+    x bf16 [T, D] (and residual, the same shape): h = bf16(x + residual), or x
+    itself without a residual; y = h * rstd * gamma is quantised as
+    fp8_quant_1x128 does it (from FP32, y is never stored). gamma [D] bf16 or
+    float32. Returns (q uint8 [T, D], scales float32 [D/128, ld_s>=T], h,
+    rstd float32 [T]); h and rstd are what fp8_rmsnorm_bwd needs."""
+    torch = _torch()
+    bf16 = torch.bfloat16
+    _dtype(x, bf16, "x")
+    _layout(x, "x")
+    T, D = x.shape
+    kind = _gamma_kind(gamma, D)
+    dev = x.device
+    if residual is not None:
+        _dtype(residual, bf16, "residual")
+        _layout(residual, "residual")
+        if residual.shape != x.shape:
+            raise ValueError("residual must be [%d, %d], got %s" % (T, D, tuple(residual.shape)))
+        h = torch.empty((T, D), dtype=bf16, device=dev) if h is None else h
+        _matrix(h, bf16, T, D, "h")
+    elif h is not None:
+        raise ValueError("h is written only with a residual")
+    q = torch.empty((T, D), dtype=torch.uint8, device=dev) if q is None else q
+    scales = torch.empty((D // 128, _pad(max(T, 1), 4)), dtype=torch.float32, device=dev) if scales is None else scales
+    rstd = torch.empty(T, dtype=torch.float32, device=dev) if rstd is None else rstd
+    _quant_out(q, scales, (T, D), D // 128, T)
+    _vector(rstd, torch.float32, T, "rstd")
+    _on_gpu((x, "x"), (gamma, "gamma"), (residual, "residual"), (h, "h"), (q, "q"), (scales, "scales"), (rstd, "rstd"))
+    rc = lib().fp8_rmsnorm(x.data_ptr(), x.stride(0), None if residual is None else residual.data_ptr(),
+                           0 if residual is None else residual.stride(0), gamma.data_ptr(), kind, T, D, eps,
+                           None if h is None else h.data_ptr(), 0 if h is None else h.stride(0), q.data_ptr(),
+                           q.stride(0), scales.data_ptr(), scales.stride(0), rstd.data_ptr(), 1 if pow2 else 0,
+                           _stream(stream))
+    _check(rc, "fp8_rmsnorm")
+    return q, scales, x if h is None else h, rstd
+
+
+def fp8_rmsnorm_t(h, rstd, gamma, qT=None, scalesT=None, stream=None, pow2=False):
+    """The norm's output of fp8_rmsnorm, recomputed from h [T, D] and rstd, as
+    fp8_quant_1x128(..., transpose=True) lays it out (T % 128 == 0): qT uint8
+    [D, T], scalesT float32 [T/128, ld_s>=D]."""
+    torch = _torch()
+    _dtype(h, torch.bfloat16, "h")
+    _layout(h, "h")
+    T, D = h.shape
+    kind = _gamma_kind(gamma, D)
+    _vector(rstd, torch.float32, T, "rstd")
+    qT = torch.empty((D, T), dtype=torch.uint8, device=h.device) if qT is None else qT
+    if scalesT is None:
+        scalesT = torch.empty((T // 128, _pad(max(D, 1), 4)), dtype=torch.float32, device=h.device)
+    _quant_out(qT, scalesT, (D, T), T // 128, D, "qT", "scalesT")
+    _on_gpu((h, "h"), (rstd, "rstd"), (gamma, "gamma"), (qT, "qT"), (scalesT, "scalesT"))
+    rc = lib().fp8_rmsnorm_t(h.data_ptr(), h.stride(0), rstd.data_ptr(), gamma.data_ptr(), kind, T, D, qT.data_ptr(),
+                             qT.stride(0), scalesT.data_ptr(), scalesT.stride(0), 1 if pow2 else 0, _stream(stream))
+    _check(rc, "fp8_rmsnorm_t")
+    return qT, scalesT
+
+
+def fp8_rmsnorm_bwd(dy, h, rstd, gamma, dres=None, dx=None, dgamma=None, stream=None):
+    """Backward pass of fp8_rmsnorm: dy bf16 [T, D] is the gradient of its
+    (dequantised) output, h and rstd what the forward call returned, dres the
+    gradient that reaches h on the residual stream. Returns (dx bf16 [T, D],
+    dgamma float32 [D]); dx is the gradient of x and of the residual alike."""
+    torch = _torch()
+    bf16 = torch.bfloat16
+    _dtype(dy, bf16, "dy")
+    _layout(dy, "dy")
+    T, D = dy.shape
+    _matrix(h, bf16, T, D, "h")
+    _vector(rstd, torch.float32, T, "rstd")
+    kind = _gamma_kind(gamma, D)
+    if dres is not None:
+        _matrix(dres, bf16, T, D, "dres")
+    dx = torch.empty((T, D), dtype=bf16, device=dy.device) if dx is None else dx
+    dgamma = torch.empty(D, dtype=torch.float32, device=dy.device) if dgamma is None else dgamma
+    _matrix(dx, bf16, T, D, "dx")
+    _vector(dgamma, torch.float32, D, "dgamma")
+    _on_gpu((dy, "dy"), (h, "h"), (rstd, "rstd"), (gamma, "gamma"), (dres, "dres"), (dx, "dx"), (dgamma, "dgamma"))
+    ws = _workspace(lib().fp8_rmsnorm_bwd_workspace(T, D), dy.device, stream)
+    rc = lib().fp8_rmsnorm_bwd(dy.data_ptr(), dy.stride(0), h.data_ptr(), h.stride(0), rstd.data_ptr(),
+                               gamma.data_ptr(), kind, None if dres is None else dres.data_ptr(),
+                               0 if dres is None else dres.stride(0), T, D, dx.data_ptr(), dx.stride(0),
+                               dgamma.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+    _check(rc, "fp8_rmsnorm_bwd")
+    return dx, dgamma
+
+
+def fp8_gated_gemm(xq, sx, wq, sw, h=None, scales=None, gu=None, save=False, stream=None, pow2=False):
+    """Gated feed-forward: h = silu(X Wg^T) * (X Wu^T) in one kernel.
+
+    xq uint8 [M, K], sx float32 [K/128, >=M] (fp8_quant_1x128 or fp8_rmsnorm);
+    wq uint8 [2I, K], sw float32 [2I/128, K/128] (fp8_quant_128x128 of the gate
+    weight's I rows on top of the up weight's). Returns (h uint8 [M, I], scales
+    float32 [I/128, ld_s>=M], gu): h quantised 1x128 for the down projection,
+    gu the two projections in bf16 [M, 2I] for fp8_gated_bwd (None unless
+    save=True or a gu buffer is given)."""
+    torch = _torch()
+    M, N2, K = _gemm_operands(FPROP, xq, sx, wq, sw)
+    if N2 % 2:
+        raise ValueError("wq must stack as many up rows as gate rows, got %d rows" % N2)
+    I = N2 // 2
+    if not sw.is_contiguous() or tuple(sw.shape) != (N2 // 128, K // 128):
+        raise ValueError("sw must be a contiguous [%d, %d], got %s" % (N2 // 128, K // 128, tuple(sw.shape)))
+    dev = xq.device
+    h = torch.empty((M, I), dtype=torch.uint8, device=dev) if h is None else h
+    scales = torch.empty((I // 128, _pad(max(M, 1), 4)), dtype=torch.float32, device=dev) if scales is None else scales
+    if gu is None and save:
+        gu = torch.empty((M, N2), dtype=torch.bfloat16, device=dev)
+    _quant_out(h, scales, (M, I), I // 128, M, "h", "scales")
+    if gu is not None:
+        _matrix(gu, torch.bfloat16, M, N2, "gu")
+    _on_gpu((xq, "xq"), (sx, "sx"), (wq, "wq"), (sw, "sw"), (h, "h"), (scales, "scales"), (gu, "gu"))
+    rc = lib().fp8_gated_gemm(xq.data_ptr(), sx.data_ptr(), xq.stride(0), sx.stride(0), wq.data_ptr(), sw.data_ptr(),
+                              wq.stride(0), M, I, K, h.data_ptr(), h.stride(0), scales.data_ptr(), scales.stride(0),
+                              None if gu is None else gu.data_ptr(), 0 if gu is None else gu.stride(0),
+                              1 if pow2 else 0, _stream(stream))
+    _check(rc, "fp8_gated_gemm")
+    return h, scales, gu
+
+
+def fp8_gated_bwd(gu, dh, q=None, scales=None, qT=None, scalesT=None, hqT=None, hscalesT=None, stream=None,
+                  pow2=False):
+    """Backward pass of the gate: gu bf16 [M, 2I] from fp8_gated_gemm, dh bf16
+    [M, I] the gradient of h (M % 128 == 0). Returns the gradient of gu
+    quantised per row (q [M, 2I], scales [2I/128, >=M]: fp8 dgrad operand) and
+    per column (qT [2I, M], scalesT [M/128, >=2I]: wgrad operand), and the
+    recomputed h per column (hqT [I, M], hscalesT [M/128, >=I]: the down
+    projection's wgrad operand)."""
+    torch = _torch()
+    u8, f32 = torch.uint8, torch.float32
+    _dtype(gu, torch.bfloat16, "gu")
+    _dtype(dh, torch.bfloat16, "dh")
+    _layout(gu, "gu")
+    _layout(dh, "dh")
+    M, I = dh.shape
+    if tuple(gu.shape) != (M, 2 * I):
+        raise ValueError("gu must be [%d, %d], got %s" % (M, 2 * I, tuple(gu.shape)))
+    dev = dh.device
+    q = torch.empty((M, 2 * I), dtype=u8, device=dev) if q is None else q
+    scales = torch.empty((2 * I // 128, _pad(max(M, 1), 4)), dtype=f32, device=dev) if scales is None else scales
+    qT = torch.empty((2 * I, M), dtype=u8, device=dev) if qT is None else qT
+    scalesT = torch.empty((M // 128, _pad(max(2 * I, 1), 4)), dtype=f32, device=dev) if scalesT is None else scalesT
+    hqT = torch.empty((I, M), dtype=u8, device=dev) if hqT is None else hqT
+    hscalesT = torch.empty((M // 128, _pad(max(I, 1), 4)), dtype=f32, device=dev) if hscalesT is None else hscalesT
+    _quant_out(q, scales, (M, 2 * I), 2 * I // 128, M)
+    _quant_out(qT, scalesT, (2 * I, M), M // 128, 2 * I, "qT", "scalesT")
+    _quant_out(hqT, hscalesT, (I, M), M // 128, I, "hqT", "hscalesT")
+    _on_gpu((gu, "gu"), (dh, "dh"), (q, "q"), (scales, "scales"), (qT, "qT"), (scalesT, "scalesT"), (hqT, "hqT"),
+            (hscalesT, "hscalesT"))
+    rc = lib().fp8_gated_bwd(gu.data_ptr(), gu.stride(0), dh.data_ptr(), dh.stride(0), M, I, q.data_ptr(), q.stride(0),
+                             scales.data_ptr(), scales.stride(0), qT.data_ptr(), qT.stride(0), scalesT.data_ptr(),
+                             scalesT.stride(0), hqT.data_ptr(), hqT.stride(0), hscalesT.data_ptr(),
+                             hscalesT.stride(0), 1 if pow2 else 0, _stream(stream))
+    _check(rc, "fp8_gated_bwd")
+    return q, scales, qT, scalesT, hqT, hscalesT
+
+
+def grad_clip(grads, max_norm, eps=1e-6, out=None, norm=None, stream=None):
+    """Scale gradients so that their global L2 norm is at most max_norm.
+
+    grads: contiguous float32 or bfloat16 CUDA tensors of any shape (views into
+    a bucket included). out: tensors to write, of the same shapes and types
+    (default: the gradients themselves). Returns (norm, out): norm float32 [2]
+    on the device holds the norm before scaling and the factor min(1, max_norm
+    / (norm + eps)); nothing is copied to the host."""
+    torch = _torch()
+    f32, bf16 = torch.float32, torch.bfloat16
+    grads = list(grads)
+    outs = grads if out is None else list(out)
+    if len(outs) != len(grads):
+        raise ValueError("out must hold one tensor per gradient")
+    if not grads:
+        raise ValueError("grads must hold at least one tensor")
+    rows = []
+    for g, o in zip(grads, outs):
+        dt = g.dtype
+        if dt is not f32 and dt is not bf16:
+            raise ValueError("gradients must be float32 or bfloat16, got %s" % dt)
+        n = g.numel()
+        if not g.is_contiguous():
+            raise ValueError("gradients must be contiguous")
+        if o is not g and (o.dtype is not dt or o.numel() != n or not o.is_contiguous()):
+            raise ValueError("out must match the gradients' shapes and types and be contiguous")
+        if not (g.is_cuda and o.is_cuda):
+            raise ValueError("grads and out must be CUDA tensors")
+        rows += (g.data_ptr(), o.data_ptr(), n, OUT_F32 if dt is f32 else OUT_BF16)
+    dev = grads[0].device
+    norm = torch.empty(2, dtype=f32, device=dev) if norm is None else norm
+    _vector(norm, f32, 2, "norm")
+    _on_gpu((norm, "norm"))
+    table = (ctypes.c_int64 * len(rows))(*rows)
+    ws = _workspace(lib().fp8fg_grad_clip_workspace(len(grads)), dev, stream)
+    rc = lib().fp8fg_grad_clip(table, len(grads), max_norm, eps, norm.data_ptr(), ws.data_ptr(), ws.numel(),
+                               _stream(stream))
+    _check(rc, "fp8fg_grad_clip")
+    return norm, outs
 
 
 def device_status(stream=None):

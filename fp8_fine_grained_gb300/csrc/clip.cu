@@ -1,0 +1,366 @@
+// Global norm of a list of gradient tensors, and the tensors scaled so that
+// it does not exceed max_norm.
+//
+//   norm = sqrt(sum over all tensors of g^2)
+//   coef = min(1, max_norm / (norm + eps))
+//   out  = g * coef
+//
+// Two streams over the data: the norm has to be known before the first
+// element is written. The first kernel leaves one FP64 partial sum per CTA;
+// every CTA of the second adds those up in the same order (a few KB from L2),
+// so the result does not depend on the schedule and no third launch is needed.
+// The second kernel walks the chunks backwards: what the first one read last
+// is still in L2.
+//
+// The tensors' pointers and sizes travel in the kernels' parameters (no device
+// table to copy). A tensor is cut into chunks of CHUNK elements whose vector
+// loads start on a 16-byte boundary of its own; the elements before the first
+// boundary belong to chunk 0. Chunks are dealt round-robin to the CTAs.
+#include <cuda_bf16.h>
+
+#include "host_common.h"
+#include "ptx.cuh"
+
+namespace fp8fg {
+namespace {
+
+constexpr int CHUNK = 8192;
+constexpr int THREADS = 256;
+constexpr int CTAS_PER_SM = 4;
+constexpr int MAX_TENSORS = 1024;  // per launch: 24 bytes + 4 each in the 32 KB of kernel parameters
+
+template <int N>
+struct Table {
+    const void *g[N];
+    void *out[N];
+    int64_t n[N];            // elements; negative: bf16
+    uint32_t first[N + 1];   // first chunk of each tensor
+    int count;
+};
+
+struct Piece {
+    const uint8_t *g;
+    uint8_t *out;
+    int64_t begin, end;  // elements of the chunk's vector part and tail
+    int head;            // elements before `begin` that belong to it (chunk 0)
+    bool bf16;
+};
+
+__host__ __device__ __forceinline__ int head_elements(const void *p, int esz)
+{
+    return (int)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / esz;
+}
+
+template <int N>
+__device__ __forceinline__ Piece piece_of(const Table<N> &tab, uint32_t chunk)
+{
+    int lo = 0, hi = tab.count;  // last tensor with first <= chunk
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (tab.first[mid] <= chunk)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    Piece q;
+    q.bf16 = tab.n[lo] < 0;
+    const int64_t n = q.bf16 ? -tab.n[lo] : tab.n[lo];
+    q.g = static_cast<const uint8_t *>(tab.g[lo]);
+    q.out = static_cast<uint8_t *>(tab.out[lo]);
+    int64_t head = head_elements(q.g, q.bf16 ? 2 : 4);
+    head = head < n ? head : n;
+    const int64_t at = (int64_t)(chunk - tab.first[lo]) * CHUNK;
+    q.head = at == 0 ? (int)head : 0;
+    q.begin = head + at;
+    q.end = q.begin + CHUNK < n ? q.begin + CHUNK : n;
+    return q;
+}
+
+__device__ __forceinline__ float load_one(const uint8_t *p, int64_t i, bool bf16)
+{
+    return bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p)[i])
+                : reinterpret_cast<const float *>(p)[i];
+}
+
+__device__ __forceinline__ void store_one(uint8_t *p, int64_t i, bool bf16, float v)
+{
+    if (bf16)
+        reinterpret_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+    else
+        reinterpret_cast<float *>(p)[i] = v;
+}
+
+__device__ __forceinline__ uint4 ld16(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ float sq16(const uint4 &v, bool bf16)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (bf16)
+            s = fmaf(bf16_lo(w[i]), bf16_lo(w[i]), fmaf(bf16_hi(w[i]), bf16_hi(w[i]), s));
+        else
+            s = fmaf(__uint_as_float(w[i]), __uint_as_float(w[i]), s);
+    }
+    return s;
+}
+
+__device__ __forceinline__ uint4 mul16(const uint4 &v, bool bf16, float c)
+{
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (bf16) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(bf16_lo(w[i]) * c, bf16_hi(w[i]) * c);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        } else {
+            w[i] = __float_as_uint(__uint_as_float(w[i]) * c);
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Sum over the block, the same in every thread and for every launch.
+__device__ __forceinline__ double block_sum(double v, double *part)
+{
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0)
+        part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w)
+        v += part[w];
+    return v;
+}
+
+constexpr int UNROLL = 8;  // 16-byte loads of a thread in flight
+
+// Squares are FP32, summed in FP32 inside a chunk (32 terms or fewer per
+// thread) and in FP64 beyond it.
+template <int N>
+__global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
+    sumsq_kernel(const __grid_constant__ Table<N> tab, double *partial)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    __shared__ double part[THREADS / 32];
+    const uint32_t chunks = tab.first[tab.count];
+    double total = 0.0;
+    for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+        const Piece q = piece_of(tab, c);
+        const int esz = q.bf16 ? 2 : 4, per = 16 / esz;
+        const int64_t len = q.end - q.begin;
+        const int vecs = len > 0 ? (int)(len / per) : 0;
+        const uint8_t *src = q.g + q.begin * esz;
+        float s = 0.0f;
+        for (int i0 = 0; i0 < vecs; i0 += UNROLL * THREADS) {
+            uint4 v[UNROLL];
+#pragma unroll
+            for (int j = 0; j < UNROLL; ++j) {
+                const int i = i0 + j * THREADS + threadIdx.x;
+                v[j] = i < vecs ? ld16(src + (int64_t)i * 16) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int j = 0; j < UNROLL; ++j)
+                s += sq16(v[j], q.bf16);
+        }
+        const int tail = len > 0 ? (int)(len - (int64_t)vecs * per) : 0;
+        if ((int)threadIdx.x < tail) {
+            const float v = load_one(q.g, q.begin + (int64_t)vecs * per + threadIdx.x, q.bf16);
+            s = fmaf(v, v, s);
+        }
+        if ((int)threadIdx.x < q.head) {
+            const float v = load_one(q.g, threadIdx.x, q.bf16);
+            s = fmaf(v, v, s);
+        }
+        total += (double)s;
+    }
+    total = block_sum(total, part);
+    if (threadIdx.x == 0)
+        partial[blockIdx.x] = total;
+}
+
+template <int N>
+__global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
+    scale_kernel(const __grid_constant__ Table<N> tab, const double *__restrict__ partial, int n_partial,
+                 float max_norm, float eps, float *norm_out)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    __shared__ double part[THREADS / 32];
+    double total = 0.0;
+    for (int i = threadIdx.x; i < n_partial; i += THREADS)
+        total += partial[i];
+    total = block_sum(total, part);
+    const float norm = (float)sqrt(total);
+    const float ratio = max_norm / (norm + eps);
+    const float coef = ratio > 1.0f ? 1.0f : ratio;  // a NaN norm gives NaN
+    if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) {
+        norm_out[0] = norm;
+        norm_out[1] = coef;
+    }
+    const uint32_t chunks = tab.first[tab.count];
+    for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+        const Piece q = piece_of(tab, chunks - 1 - c);
+        if (coef == 1.0f && q.out == q.g)
+            continue;
+        const int esz = q.bf16 ? 2 : 4, per = 16 / esz;
+        const int64_t len = q.end - q.begin;
+        // vector stores need the output on the input's 16-byte grid
+        const bool same = ((reinterpret_cast<uintptr_t>(q.g) ^ reinterpret_cast<uintptr_t>(q.out)) & 15) == 0;
+        const int vecs = len > 0 && same ? (int)(len / per) : 0;
+        const uint8_t *src = q.g + q.begin * esz;
+        uint8_t *dst = q.out + q.begin * esz;
+        for (int i0 = 0; i0 < vecs; i0 += UNROLL * THREADS) {
+            uint4 v[UNROLL];
+#pragma unroll
+            for (int j = 0; j < UNROLL; ++j) {
+                const int i = i0 + j * THREADS + threadIdx.x;
+                if (i < vecs)
+                    v[j] = ld16(src + (int64_t)i * 16);
+            }
+#pragma unroll
+            for (int j = 0; j < UNROLL; ++j) {
+                const int i = i0 + j * THREADS + threadIdx.x;
+                if (i < vecs)
+                    *reinterpret_cast<uint4 *>(dst + (int64_t)i * 16) = mul16(v[j], q.bf16, coef);
+            }
+        }
+        for (int64_t i = q.begin + (int64_t)vecs * per + threadIdx.x; i < q.end; i += THREADS)
+            store_one(q.out, i, q.bf16, load_one(q.g, i, q.bf16) * coef);
+        if ((int)threadIdx.x < q.head)
+            store_one(q.out, threadIdx.x, q.bf16, load_one(q.g, threadIdx.x, q.bf16) * coef);
+    }
+}
+
+int64_t grid_cap()
+{
+    const int sms = sm_count();
+    return (int64_t)(sms > 0 ? sms : 1) * CTAS_PER_SM;
+}
+
+int64_t chunks_of(const fp8fg_grad &t)
+{
+    const int64_t body = t.n - head_elements(t.g, t.kind == FP8FG_OUT_BF16 ? 2 : 4);
+    return body > CHUNK ? (body + CHUNK - 1) / CHUNK : 1;
+}
+
+// Tensors [at, at + take) of one launch; their chunks fit in 31 bits
+template <int N>
+void fill(Table<N> &tab, const fp8fg_grad *t, int take)
+{
+    uint32_t first = 0;
+    for (int i = 0; i < take; ++i) {
+        tab.g[i] = t[i].g;
+        tab.out[i] = t[i].out;
+        tab.n[i] = t[i].kind == FP8FG_OUT_BF16 ? -t[i].n : t[i].n;
+        tab.first[i] = first;
+        if (t[i].n > 0)
+            first += (uint32_t)chunks_of(t[i]);
+    }
+    tab.first[take] = first;
+    tab.count = take;
+}
+
+// The smaller parameter block of a short list copies faster at the launch.
+template <int N>
+int launch_sumsq(const fp8fg_grad *t, int take, double *partial, int *used, cudaStream_t s)
+{
+    Table<N> tab;
+    fill(tab, t, take);
+    const int64_t chunks = tab.first[take];
+    *used = (int)(chunks < grid_cap() ? (chunks > 0 ? chunks : 1) : grid_cap());
+    return launch_pss(sumsq_kernel<N>, dim3((unsigned)*used), THREADS, 0, s, tab, partial);
+}
+
+template <int N>
+int launch_scale(const fp8fg_grad *t, int take, const double *partial, int n_partial, float max_norm, float eps,
+                 float *norm, cudaStream_t s)
+{
+    Table<N> tab;
+    fill(tab, t, take);
+    const int64_t chunks = tab.first[take];
+    const int64_t grid = chunks < grid_cap() ? (chunks > 0 ? chunks : 1) : grid_cap();
+    return launch_pss(scale_kernel<N>, dim3((unsigned)grid), THREADS, 0, s, tab, partial, n_partial, max_norm, eps, norm);
+}
+
+}  // namespace
+}  // namespace fp8fg
+
+using namespace fp8fg;
+
+extern "C" int64_t fp8fg_grad_clip_workspace(int64_t count)
+{
+    if (count < 0)
+        return 0;
+    const int64_t launches = count > 0 ? (count + MAX_TENSORS - 1) / MAX_TENSORS : 1;
+    return launches * grid_cap() * 8;
+}
+
+extern "C" int fp8fg_grad_clip(const fp8fg_grad *grads, int64_t count, float max_norm, float eps, float *norm,
+                               void *workspace, int64_t workspace_bytes, void *stream)
+{
+    if (count < 0 || count >= (1ll << 20) || !(max_norm >= 0.0f) || !(eps >= 0.0f) || !norm || !workspace ||
+        (count > 0 && !grads))
+        return FP8FG_EINVAL;
+    if ((reinterpret_cast<uintptr_t>(norm) & 3u) != 0 || (reinterpret_cast<uintptr_t>(workspace) & 7u) != 0)
+        return FP8FG_EALIGN;
+    for (int64_t i = 0; i < count; ++i) {
+        const fp8fg_grad &t = grads[i];
+        if ((t.kind != FP8FG_OUT_F32 && t.kind != FP8FG_OUT_BF16) || t.n < 0 || t.n >= (1ll << 42) ||
+            (t.n > 0 && (!t.g || !t.out)))
+            return FP8FG_EINVAL;
+        const uintptr_t mask = t.kind == FP8FG_OUT_BF16 ? 1u : 3u;
+        if (t.n > 0 && (((reinterpret_cast<uintptr_t>(t.g) | reinterpret_cast<uintptr_t>(t.out)) & mask) != 0))
+            return FP8FG_EALIGN;
+    }
+    if (!device_supported())
+        return FP8FG_EUNSUPPORTED;
+    if (workspace_bytes < fp8fg_grad_clip_workspace(count))
+        return FP8FG_EINVAL;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    double *partial = static_cast<double *>(workspace);
+    // launches of at most MAX_TENSORS tensors and 2^31 chunks
+    int n_partial = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+        int64_t at = 0;
+        do {
+            const int take = (int)(count - at < MAX_TENSORS ? count - at : MAX_TENSORS);
+            int64_t chunks = 0;
+            for (int i = 0; i < take; ++i)
+                chunks += chunks_of(grads[at + i]);
+            if (chunks >= (1ll << 31))
+                return FP8FG_EINVAL;
+            int rc;
+            if (pass == 0) {
+                int used = 0;
+                rc = take <= 64 ? launch_sumsq<64>(grads + at, take, partial + n_partial, &used, s)
+                                : (take <= 256 ? launch_sumsq<256>(grads + at, take, partial + n_partial, &used, s)
+                                               : launch_sumsq<MAX_TENSORS>(grads + at, take, partial + n_partial, &used, s));
+                n_partial += used;
+            } else {
+                float *out = at == 0 ? norm : nullptr;
+                rc = take <= 64 ? launch_scale<64>(grads + at, take, partial, n_partial, max_norm, eps, out, s)
+                                : (take <= 256
+                                       ? launch_scale<256>(grads + at, take, partial, n_partial, max_norm, eps, out, s)
+                                       : launch_scale<MAX_TENSORS>(grads + at, take, partial, n_partial, max_norm, eps,
+                                                                   out, s));
+            }
+            if (rc != FP8FG_OK)
+                return rc;
+            at += take;
+        } while (at < count);
+    }
+    return FP8FG_OK;
+}

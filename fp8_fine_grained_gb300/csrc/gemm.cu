@@ -43,7 +43,9 @@
 #include <cuda_bf16.h>
 
 #include "group_rule.cuh"
+#include "gate.cuh"
 #include "group_tiles.cuh"
+#include "gated_args.h"
 #include "host_common.h"
 #include "ptx.cuh"
 #include "tensor_map.h"
@@ -84,11 +86,18 @@ constexpr uint32_t STAGE_C_BYTES = 32 * 64;
 // GROUPED: MoE experts, A rows gathered through a row index by warps 2..3.
 // GROUPED_C: MoE experts, A rows already in expert order (TMA tiles). Two
 // instantiations, so that neither carries the other's registers.
-enum Mode { FPROP = 0, DGRAD = 1, WGRAD = 2, GROUPED = 3, GROUPED_C = 4 };
+// GATED: the gate and up projections of a gated feed-forward. B is the stacked
+// weight [2I][K] and a tile's 256 B rows are the gate and up rows of 128
+// columns of h, interleaved in runs of 64 (gate c..c+63, up c..c+63, gate
+// c+64.., up c+64..): a promotion thread's 128 columns then hold both factors
+// of 64 columns of h, and the gate is applied in registers.
+enum Mode { FPROP = 0, DGRAD = 1, WGRAD = 2, GROUPED = 3, GROUPED_C = 4, GATED = 5 };
 // Output element: FP32, bf16 (RNE), or E4M3 with 1x128 scales along N (the
 // bf16 value of each element quantised by the group rule, i.e. what
 // fp8_quant_1x128 of the bf16 output would write).
 enum Out { OUT_F32 = 0, OUT_BF16 = 1, OUT_E4M3 = 2 };
+constexpr int GATED_RUN = 64;                 // gate or up rows of one TMA box
+constexpr int GATED_BN = BN / 2;              // columns of h per tile
 constexpr bool is_grouped(int mode) { return mode == GROUPED || mode == GROUPED_C; }
 
 struct Params {
@@ -122,6 +131,11 @@ struct Params {
     // relative to a full one, in percent, divides the CTAs between the two
     int skinny_rows;
     int skinny_cost_pct;
+    // gated mode (N = I, the columns of h): the two projections in bf16,
+    // [M][ld_gu] with the up projection I columns on; nullptr: not written
+    uint16_t *gu;
+    int64_t ld_gu;
+    int out_pow2;  // scale rule of h
 };
 
 // Scale slot of one pipeline stage: the A row scales of the block (a box of
@@ -165,10 +179,15 @@ template <int MODE> struct SmemLayout {
     static constexpr uint32_t tok_end = tok_off + (MODE == GROUPED ? 4 * BM : 0);
     static constexpr uint32_t prefix_off = tok_end;                             // grouped: tile prefix
     static constexpr uint32_t prefix_end = prefix_off + (is_grouped(MODE) ? 4 * (MAX_EXPERTS + 1) : 0);
-    static constexpr uint32_t total = prefix_end;
+    // GATED: per TMEM lane quarter, the barrier and the two halves' row maxima
+    // (double-buffered) that the quarter's two promotion warps exchange
+    static constexpr uint32_t xbar_off = (prefix_end + 7) & ~7u;
+    static constexpr uint32_t xmax_off = xbar_off + (MODE == GATED ? 8 * 4 : 0);
+    static constexpr uint32_t total = xmax_off + (MODE == GATED ? 2 * 2 * 4 * BM : 0);
 };
 static_assert(SmemLayout<FPROP>::total <= 232448, "shared memory budget");
 static_assert(SmemLayout<WGRAD>::total <= 232448, "shared memory budget");
+static_assert(SmemLayout<GATED>::total <= 232448, "shared memory budget");
 static_assert(SmemLayout<GROUPED>::total <= 232448, "shared memory budget");
 static_assert(SmemLayout<GROUPED_C>::total <= 232448, "shared memory budget");
 
@@ -208,7 +227,9 @@ template <int MODE>
 __device__ __forceinline__ const float *weight_scale(const Params &p, const Tile &tl, int kb, int h)
 {
     const int64_t nb = tl.n0 / 128 + h;
-    if constexpr (MODE == FPROP)
+    if constexpr (MODE == GATED)  // h = 0: the gate block, 1: the up block
+        return p.sB + (tl.n0 / 128 + h * (p.N / 128)) * p.ld_sB + kb;
+    else if constexpr (MODE == FPROP)
         return p.sB + nb * p.ld_sB + kb;
     else if constexpr (MODE == DGRAD)
         return p.sB + (int64_t)kb * p.ld_sB + nb;
@@ -239,7 +260,7 @@ __device__ __forceinline__ Tile decode_tile(int64_t t, const Params &p, const in
         const int64_t g = (nb - first) < p.band ? (nb - first) : p.band;
         const int64_t fast = first + r % g, slow = r / g;
         tl.m0 = (p.n_major ? slow : fast) * BM;
-        tl.n0 = (p.n_major ? fast : slow) * BN;
+        tl.n0 = (p.n_major ? fast : slow) * (MODE == GATED ? GATED_BN : BN);
         tl.row_end = p.M;
         tl.expert = 0;
     }
@@ -540,6 +561,86 @@ __device__ __forceinline__ void skinny_roles(const CUtensorMap *tmX, const CUten
     }
 }
 
+// ----------------------------------------------------------------- gated ----
+// Epilogue of a GATED tile for one promotion warp: acc[0..31] are the gate
+// sums and acc[32..63] the up sums of the thread's row at columns col0 ..
+// col0+63 of h. Stores the two projections in bf16 when asked for, then
+//   h = gate * sigmoid(gate) * up        (silu_mul)
+// in FP32 and its E4M3 codes. The 128 columns of a scale group lie in the two
+// warps of the row's lane quarter: they exchange their row maxima through
+// shared memory, ordered by a barrier of the pair. A warp can be one exchange
+// ahead of its partner at most, so two sets of maxima suffice. All stores pass
+// through the warp's staging block as in the other epilogues. Returns false
+// when the (bounded) wait for the partner ran out.
+template <class L>
+__device__ __forceinline__ bool gated_epilogue(const Params &p, uint8_t *smem, float2 (&acc)[64], int64_t row,
+                                               bool row_ok, const Tile &tl, int64_t col0, int ew, int lane,
+                                               uint32_t xphase, const WaitCtl &wc)
+{
+    uint8_t *const stg = smem + L::stage_c_off + ew * STAGE_C_BYTES;
+    uint8_t *const w_row = stg + lane * 64;
+    const int w_sw = (lane >> 1) & 3;
+    const int cc = lane & 3;
+    const uint8_t *const r_ptr = stg + (lane >> 2) * 64 + ((cc ^ ((lane >> 3) & 3)) << 4);
+    const int64_t rrow0 = row - lane + (lane >> 2);
+    // 64 bytes of each of the warp's rows, from `o` to `base` (of row rrow0)
+    auto store_piece = [&](const uint4 (&o)[4], uint8_t *base, int64_t pitch) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<uint4 *>(w_row + ((c ^ w_sw) << 4)) = o[c];
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(r_ptr + i * 512);
+            if (rrow0 + 8 * i < tl.row_end)
+                *reinterpret_cast<uint4 *>(base + 8 * i * pitch + cc * 16) = v;
+        }
+        __syncwarp();
+    };
+    if (p.gu) {
+        uint8_t *const out = reinterpret_cast<uint8_t *>(p.gu + rrow0 * p.ld_gu + col0);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            uint4 o[4];
+            uint32_t *w = reinterpret_cast<uint32_t *>(o);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const __nv_bfloat162 b = __float22bfloat162_rn(acc[16 * q + k]);
+                w[k] = *reinterpret_cast<const uint32_t *>(&b);
+            }
+            store_piece(o, out + (q >> 1) * p.N * 2 + (q & 1) * 64, p.ld_gu * 2);
+        }
+    }
+    float amax = 0.0f;
+#pragma unroll
+    for (int a = 0; a < 32; ++a) {
+        acc[a].x = silu_mul(acc[a].x, acc[32 + a].x);
+        acc[a].y = silu_mul(acc[a].y, acc[32 + a].y);
+        amax = fmaxf(amax, fmaxf(fabsf(acc[a].x), fabsf(acc[a].y)));
+    }
+    const int quarter = ew & 3, half = ew >> 2;
+    float *const xmax = reinterpret_cast<float *>(smem + L::xmax_off) + xphase * (2 * BM) + quarter * 32 + lane;
+    const uint32_t xbar = smem_u32(smem) + L::xbar_off + 8 * quarter;
+    xmax[half * BM] = amax;
+    __syncwarp();
+    if (lane == 0)
+        mbar_arrive(xbar);
+    if (!__all_sync(0xffffffffu, mbar_wait(xbar, xphase, wc, FP8FG_ETIMEOUT)))
+        return false;
+    amax = fmaxf(amax, xmax[(half ^ 1) * BM]);
+    const ScalePair sp = p.out_pow2 ? group_scale_pow2(amax) : group_scale(amax);
+    if (half == 0 && row_ok)
+        p.sC[(tl.n0 / 128) * p.ld_sC + row] = sp.s;
+    uint4 o[4];
+    uint32_t *w = reinterpret_cast<uint32_t *>(o);
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+        w[k] = cvt_e4m3x2(__fmul_rn(acc[2 * k].x, sp.inv), __fmul_rn(acc[2 * k].y, sp.inv)) |
+               (cvt_e4m3x2(__fmul_rn(acc[2 * k + 1].x, sp.inv), __fmul_rn(acc[2 * k + 1].y, sp.inv)) << 16);
+    store_piece(o, static_cast<uint8_t *>(p.C) + rrow0 * p.ldc + col0, p.ldc);
+    return true;
+}
+
 template <int MODE, int OUT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -590,6 +691,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // needs, which a parity wait cannot tell apart
         for (int s = 0; s < STAGES; ++s)
             mbar_init(tempty_bar + 8 * s, EPI_WARPS);
+        if constexpr (MODE == GATED)
+            for (int qd = 0; qd < 4; ++qd)
+                mbar_init(sbase + L::xbar_off + 8 * qd, 2);
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmA);
@@ -709,7 +813,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                             // the weight-block scales of the tile's two column
                             // halves (4-byte copies: one FP32 per block and half)
                             cp_async4(sc_dst + SS::b_off, weight_scale<MODE>(p, tl, kb, 0));
-                            if (tl.n0 + 128 < p.N)
+                            if (MODE == GATED || tl.n0 + 128 < p.N)
                                 cp_async4(sc_dst + SS::b_off + 4, weight_scale<MODE>(p, tl, kb, 1));
                             cp_async_mbar_arrive_noinc(fb);
                         }
@@ -729,6 +833,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                             tma_load_2d(b_dst, &tmB, (int32_t)tl.n0, kb * BK, fb);
                             if (second_half)
                                 tma_load_2d(b_dst + B_STAGE_BYTES / 2, &tmB, (int32_t)tl.n0 + 128, kb * BK, fb);
+                        } else if constexpr (MODE == GATED) {
+#pragma unroll
+                            for (int r = 0; r < BN / GATED_RUN; ++r)
+                                tma_load_2d(b_dst + r * GATED_RUN * BK, &tmB, kb * BK,
+                                            (int32_t)(tl.n0 + (r & 1) * p.N + (r >> 1) * GATED_RUN), fb);
                         } else {
                             tma_load_2d(b_dst, &tmB, kb * BK, (int32_t)tl.n0, fb);
                         }
@@ -846,12 +955,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         float *wscale = reinterpret_cast<float *>(smem + L::stage_c_off + ew * STAGE_C_BYTES);
         uint32_t buf = 0, tphase = 0;        // TMEM partial buffer
         uint32_t stage = 0, phase = 0;       // pipeline stage holding the block's scales
+        uint32_t xphase = 0;                 // GATED: exchange of the row maxima
         bool ok = true;
         for (int64_t t = sched->first; t < sched->count && ok; t += sched->stride) {
             const Tile tl = decode_tile<MODE>(t, p, prefix);
             const int64_t row = tl.m0 + row_in_tile;  // A row (dense) / output row (grouped)
             const bool row_ok = row < tl.row_end;
-            const int64_t col0 = tl.n0 + half * 128;
+            const int64_t col0 = tl.n0 + half * (MODE == GATED ? GATED_RUN : 128);
             const bool cols_ok = col0 < p.N;
             // this thread's row scale inside a stage's slot (TMA boxes start
             // at the 4-aligned row at or below the tile's first row)
@@ -879,7 +989,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 // gradient) the half's 128 column scales, copied to the
                 // warp's own shared block for the fold
                 const float *bslot = reinterpret_cast<const float *>(slot + SS::b_off);
-                const float sb = MODE == WGRAD ? 0.0f : bslot[half];
+                const float sb = MODE == WGRAD ? 0.0f : bslot[MODE == GATED ? 0 : half];
+                // GATED: the thread's first 64 columns are gate, the others up
+                const float sb_up = MODE == GATED ? bslot[1] : sb;
                 if constexpr (MODE == WGRAD)
                     reinterpret_cast<float4 *>(wscale)[lane] = reinterpret_cast<const float4 *>(bslot + half * 128)[lane];
                 got = mbar_wait(tfull_bar + 8 * buf, tphase, wc, FP8FG_ETIMEOUT);
@@ -897,8 +1009,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + buf * BN + half * 128;
                 const float sab = sa * sb;
                 const float2 s2 = make_float2(sab, sab);
+                const float2 s2_up = make_float2(sa * sb_up, sa * sb_up);
                 const float2 sa2 = make_float2(sa, sa);
                 // fold one 16-column chunk c (held in r) into the sums
+                constexpr int HALF_CHUNKS = GATED_RUN / CHUNK;
                 auto fold = [&](int c, const uint32_t(&r)[CHUNK]) {
 #pragma unroll
                     for (int j = 0; j < CHUNK / 2; ++j) {
@@ -908,7 +1022,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                             const float2 sc = reinterpret_cast<const float2 *>(wscale)[a];
                             acc[a] = __ffma2_rn(pv, __fmul2_rn(sa2, sc), acc[a]);
                         } else {
-                            acc[a] = __ffma2_rn(pv, s2, acc[a]);
+                            acc[a] = __ffma2_rn(pv, MODE == GATED && c >= HALF_CHUNKS ? s2_up : s2, acc[a]);
                         }
                     }
                 };
@@ -964,6 +1078,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             // per instruction and stores those runs. Rows past the tile's
             // group (the next expert, or past M) are skipped.
             float qinv = 1.0f;
+            if constexpr (MODE == GATED) {
+                ok = gated_epilogue<L>(p, smem, acc, row, row_ok, tl, col0, ew, lane, xphase, wc);
+                xphase ^= 1;
+                continue;
+            }
             if constexpr (OUT == OUT_E4M3) {
                 // round to bf16 in place (the values a bf16 store keeps), then
                 // the group rule over this thread's 128 columns: one 1x128
@@ -1313,6 +1432,44 @@ int gemm_entry(int mode, const uint8_t *A, const float *sA, int64_t lda, int64_t
 }
 
 }  // namespace
+}  // namespace fp8fg
+
+namespace fp8fg {
+
+// The 128-row tiles of fp8_gated_gemm (gemm_gated.cu checks the arguments).
+int gated_gemm_tiles(const GatedArgs &g, cudaStream_t s)
+{
+    Params p{};
+    p.M = g.M;
+    p.N = g.I;
+    p.K = g.K;
+    p.sA = g.sx;
+    p.ld_sA = g.ld_sx;
+    p.sB = g.sw;
+    p.ld_sB = g.K / BK;
+    p.C = g.h;
+    p.ldc = g.ldh;
+    p.sC = g.sh;
+    p.ld_sC = g.ld_sh;
+    p.gu = g.gu;
+    p.ld_gu = g.ld_gu;
+    p.out_pow2 = g.pow2;
+    p.num_m_tiles = (g.M + BM - 1) / BM;
+    p.num_n_tiles = g.I / GATED_BN;
+    choose_raster(p, FPROP);
+    if (!fill_runtime(p))
+        return FP8FG_ECUDA;
+    Maps m;
+    if (!make_map(&m.a, g.xq, (uint64_t)g.K, (uint64_t)g.M, (uint64_t)g.ldx, BK, BM) ||
+        !make_map(&m.b, g.wq, (uint64_t)g.K, (uint64_t)(2 * g.I), (uint64_t)g.ldw, BK, GATED_RUN) ||
+        !make_map_f32_row(&m.sa, g.sx, (uint64_t)g.M, (uint64_t)(g.K / BK), (uint64_t)g.ld_sx, SA_BOX))
+        return FP8FG_ECUDA;
+    m.sb = m.sa;  // unused
+    const int64_t tiles = p.num_m_tiles * p.num_n_tiles;
+    const int sms = sm_count();
+    return launch<GATED, OUT_E4M3>(m, p, (int)(tiles < sms ? tiles : sms), s);
+}
+
 }  // namespace fp8fg
 
 extern "C" int fp8_gemm_blockscaled(int mode, const uint8_t *A, const float *sA, int64_t lda, int64_t ld_sA,

@@ -39,4 +39,27 @@ inline int launch_status()
     return e == cudaSuccess ? FP8FG_OK : FP8FG_ECUDA;
 }
 
+// Launch with programmatic stream serialization: the grid may start while the
+// previous kernel's last CTAs run, so the kernel waits (griddep_wait) before
+// it touches memory that an earlier kernel of the stream reads or writes.
+template <typename... KArgs, typename... Args>
+int launch_pss(void (*k)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t s, const Args &...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, k, KArgs(args)...) != cudaSuccess) {
+        cudaGetLastError();
+        return FP8FG_ECUDA;
+    }
+    return launch_status();
+}
+
 }  // namespace fp8fg

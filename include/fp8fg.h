@@ -446,6 +446,142 @@ FP8FG_API int fp8_grouped_gemm_mx(const uint8_t *Xq, const float *sX, int64_t ld
                          void *Y, int out, int64_t ldy, void *stream);
 
 /* ---------------------------------------------------------------------
+ * The operators between the GEMMs of a gated MLP block. The pages describe
+ * the FP8 products and leave the norm, the gate and the clipping to the
+ * surrounding framework; these are the standard definitions of a
+ * transformer's MLP block, with the quantisation of the entry points above
+ * fused in. Their FP32 results are quantised directly (one rounding per
+ * code), never rounded to bf16 in between. `pow2` = 1 selects the
+ * power-of-two scale rule of the microscaling variant (0: the pages' rule).
+ *
+ * fp8_rmsnorm: residual addition, root-mean-square norm and 1x128
+ * quantisation.
+ *   h[t]    = bf16(x[t] + residual[t])    (residual NULL: h = x, not written)
+ *   rstd[t] = (mean_j h[t][j]^2 + eps)^-1/2
+ *   y[t][j] = h[t][j] * rstd[t] * gamma[j]
+ *   q, scales: the 1x128 codes and scales of y.
+ *   x        bf16 [T][ldx]; residual bf16 [T][ldr] or NULL.
+ *   gamma    [D], bf16 or FP32 per gamma_kind (FP8FG_OUT_BF16 / _F32).
+ *   eps      finite, > 0.
+ *   h        bf16 [T][ldh], written only with a residual; may be x or the
+ *            residual itself (in place).
+ *   q        E4M3 [T][ldq]; scales FP32 [D/128][ld_s], ld_s >= T (the GEMM's
+ *            layout); rstd FP32 [T] (the backward pass reads it).
+ *   D % 128 == 0, D <= 18432; T >= 0 arbitrary. Squares are summed in FP32.
+ *   Alignment: x, residual, gamma, h, q, scales 16-byte aligned; ldx, ldr,
+ *   ldh % 8 == 0, ldq % 16 == 0, ld_s % 4 == 0; rstd 4-byte aligned.
+ * ------------------------------------------------------------------- */
+FP8FG_API int fp8_rmsnorm(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *gamma,
+                          int gamma_kind, int64_t T, int64_t D, float eps, void *h, int64_t ldh, uint8_t *q,
+                          int64_t ldq, float *scales, int64_t ld_s, float *rstd, int pow2, void *stream);
+
+/* ---------------------------------------------------------------------
+ * fp8_rmsnorm_t: the norm's output y, recomputed from h and rstd, in the
+ * layout of fp8_quant_1x128 with transpose = 1 (groups of 128 rows of a
+ * column): the activation operand of the weight gradient.
+ *   qT      E4M3 [D][ldqT], ldqT >= T; scalesT FP32 [T/128][ld_sT], ld_sT >= D.
+ *   T % 128 == 0, D % 128 == 0, D <= 18432. Alignment as fp8_rmsnorm.
+ * ------------------------------------------------------------------- */
+FP8FG_API int fp8_rmsnorm_t(const void *h, int64_t ldh, const float *rstd, const void *gamma, int gamma_kind,
+                            int64_t T, int64_t D, uint8_t *qT, int64_t ldqT, float *scalesT, int64_t ld_sT,
+                            int pow2, void *stream);
+
+/* ---------------------------------------------------------------------
+ * fp8_rmsnorm_bwd: backward pass of fp8_rmsnorm (the quantisation is passed
+ * through). With a = dy * gamma and c = mean_j(a[t][j] * h[t][j]) * rstd[t]:
+ *   dx[t][j]  = rstd[t] * (a[t][j] - h[t][j] * rstd[t] * c) (+ dres[t][j])
+ *   dgamma[j] = sum_t dy[t][j] * h[t][j] * rstd[t]
+ * dx is the gradient of x and of the residual alike.
+ *   dy      bf16 [T][lddy]; h bf16 [T][ldh] and rstd FP32 [T] of the forward
+ *           call; dres bf16 [T][lddres] or NULL: the gradient that reaches h
+ *           on the residual stream.
+ *   dx      bf16 [T][lddx] (may be dy or dres itself); dgamma FP32 [D].
+ *   workspace  16-byte aligned, at least fp8_rmsnorm_bwd_workspace(T, D) bytes
+ *           on the current device; its contents need not be kept.
+ *   The sums run in a fixed order: the result does not vary between calls.
+ *   T == 0 sets dgamma to zero. Sizes and alignment as fp8_rmsnorm.
+ * ------------------------------------------------------------------- */
+FP8FG_API int64_t fp8_rmsnorm_bwd_workspace(int64_t T, int64_t D);
+FP8FG_API int fp8_rmsnorm_bwd(const void *dy, int64_t lddy, const void *h, int64_t ldh, const float *rstd,
+                              const void *gamma, int gamma_kind, const void *dres, int64_t lddres, int64_t T,
+                              int64_t D, void *dx, int64_t lddx, float *dgamma, void *workspace,
+                              int64_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------
+ * fp8_gated_gemm: gate and up projections, SiLU and product in one kernel.
+ *   G = fprop(X, Wg), U = fprop(X, Wu), h = G * sigmoid(G) * U
+ * with the products, promotion and operand layouts of fp8_gemm_blockscaled
+ * (FP8FG_FPROP); h is quantised 1x128 (what the down projection reads).
+ *   xq      E4M3 [M][ldx], sx FP32 [K/128][ld_sx] (ld_sx >= M).
+ *   wq      E4M3 [2I][ldw]: the I gate rows, then the I up rows, each
+ *           quantised in 128x128 blocks; sw FP32 [2I/128][K/128], dense.
+ *   h       E4M3 [M][ldh]; scales FP32 [I/128][ld_s], ld_s >= M.
+ *   gu      bf16 [M][ldgu] or NULL: G in columns 0..I-1 and U in columns
+ *           I..2I-1, rounded to nearest even (fp8_gated_bwd reads them).
+ *   K % 128 == 0, I % 128 == 0, M >= 0 arbitrary. pow2 concerns h's scales.
+ *   Alignment: xq, sx, wq, h, scales, gu 16-byte aligned, sw 4-byte aligned;
+ *   ldx, ldw, ldh % 16 == 0; ld_sx, ld_s % 4 == 0; ldgu % 8 == 0.
+ * ------------------------------------------------------------------- */
+FP8FG_API int fp8_gated_gemm(const uint8_t *xq, const float *sx, int64_t ldx, int64_t ld_sx, const uint8_t *wq,
+                             const float *sw, int64_t ldw, int64_t M, int64_t I, int64_t K, uint8_t *h,
+                             int64_t ldh, float *scales, int64_t ld_s, void *gu, int64_t ldgu, int pow2,
+                             void *stream);
+
+/* ---------------------------------------------------------------------
+ * fp8_gated_bwd: backward pass of the gate, quantised for the GEMMs that
+ * follow. With dh the gradient of h, sg = sigmoid(G) and a = G * sg:
+ *   dG = dh * U * (sg + a * (1 - sg)),  dU = dh * a,  h = a * U
+ *   q, scales      [dG dU] 1x128: E4M3 [M][ldq], FP32 [2I/128][ld_s]
+ *                  (fp8_gemm_blockscaled FP8FG_DGRAD against wq gives dX)
+ *   qT, scalesT    the same grouped along the rows and transposed: E4M3
+ *                  [2I][ldqT], FP32 [M/128][ld_sT] (FP8FG_WGRAD against the
+ *                  transposed input gives the stacked weight's gradient)
+ *   hqT, hscalesT  h grouped along the rows and transposed: E4M3 [I][ldhT],
+ *                  FP32 [M/128][ld_hsT] (FP8FG_WGRAD gives the down
+ *                  projection's gradient)
+ *   gu      bf16 [M][ldgu] as fp8_gated_gemm writes it; dh bf16 [M][lddh].
+ *   M % 128 == 0, I % 128 == 0. Alignment: every pointer 16-byte aligned;
+ *   ldgu, lddh % 8 == 0; ldq, ldqT, ldhT % 16 == 0; ld_s, ld_sT, ld_hsT % 4
+ *   == 0.
+ * ------------------------------------------------------------------- */
+FP8FG_API int fp8_gated_bwd(const void *gu, int64_t ldgu, const void *dh, int64_t lddh, int64_t M, int64_t I,
+                            uint8_t *q, int64_t ldq, float *scales, int64_t ld_s, uint8_t *qT, int64_t ldqT,
+                            float *scalesT, int64_t ld_sT, uint8_t *hqT, int64_t ldhT, float *hscalesT,
+                            int64_t ld_hsT, int pow2, void *stream);
+
+/* ---------------------------------------------------------------------
+ * fp8fg_grad_clip: global L2 norm of a list of gradients, and the gradients
+ * scaled to at most max_norm.
+ *   norm = sqrt(sum of g^2 over all tensors), coef = min(1, max_norm / (norm
+ *   + eps)), out = g * coef (one FP32 product, rounded to the tensor's type).
+ *   grads   HOST array of `count` (< 2^20) descriptors, read before the call
+ *           returns. g and out are device pointers aligned to their element
+ *           (not more: views into a flat bucket are fine), out == g scales in
+ *           place (nothing is written when coef is 1); otherwise the outputs
+ *           overlap no input. n == 0 is allowed.
+ *   norm    FP32 [2], device: the norm and coef.
+ *   workspace  8-byte aligned, at least fp8fg_grad_clip_workspace(count)
+ *           bytes on the current device.
+ *   Squares are FP32 and are added up in FP32 over at most 32 elements of a
+ *   thread, in FP64 beyond; the order is fixed, so the result does not vary
+ *   between calls. Elements beyond 1.8e19 in magnitude give an infinite norm
+ *   (coef 0), a NaN gives NaN everywhere; elements below 1e-23 count as zero
+ *   in the norm.
+ *   max_norm >= 0, eps >= 0.
+ * ------------------------------------------------------------------- */
+typedef struct {
+    const void *g;
+    void *out;
+    int64_t n;       /* elements */
+    int32_t kind;    /* FP8FG_OUT_F32 or FP8FG_OUT_BF16 */
+    int32_t unused;
+} fp8fg_grad;
+
+FP8FG_API int64_t fp8fg_grad_clip_workspace(int64_t count);
+FP8FG_API int fp8fg_grad_clip(const fp8fg_grad *grads, int64_t count, float max_norm, float eps, float *norm,
+                              void *workspace, int64_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------
  * Status and diagnostics (no counterpart on the pages).
  * ------------------------------------------------------------------- */
 
@@ -461,7 +597,8 @@ FP8FG_API int fp8fg_device_status(void *stream);
 FP8FG_API int fp8fg_version(void);
 
 /* Test hook: when `skip` != 0, the next fp8_gemm_blockscaled, fp8_gemm_mx,
- * fp8_grouped_gemm_mx or fp8_quant_1x128_dual(_pow2) launch on the current
+ * fp8_grouped_gemm_mx, fp8_quant_1x128_dual(_pow2), fp8_gated_gemm or
+ * fp8_gated_bwd launch on the current
  * device withholds its first operand load (a fp8_grouped_gemm launch
  * clears the request without using it), so the consumers' bounded waits
  * run out and the launch reports FP8FG_ETIMEOUT. One-shot; returns
