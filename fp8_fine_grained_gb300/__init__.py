@@ -23,6 +23,8 @@ plus the convenience wrappers fprop / dgrad / wgrad and device_status().
 """
 import ctypes
 import os
+from array import array
+from operator import attrgetter
 
 FPROP, DGRAD, WGRAD = 0, 1, 2
 OUT_F32, OUT_BF16 = 0, 1
@@ -107,9 +109,12 @@ def _torch():
 
 
 def _stream(stream):
+    """Handle of the given stream, or of the current device's current stream
+    (by the raw query: 0.3 us where building a Stream object takes 3 us)."""
+    if stream is not None:
+        return stream.cuda_stream
     torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _ptr(t):
@@ -583,16 +588,25 @@ def fp8_moe_combine(y, dest, w, out_dtype=None, out=None, stream=None):
 
 
 # ------------------------------------------- between a gated MLP's GEMMs ----
+# These calls are short (a decoding step spends more time here than on the
+# GPU), so each tensor is looked at once: _matrix and _vector check it and
+# return what the library needs.
 
 def _matrix(t, dtype, rows, cols, name):
-    """A 2-D row-major tensor of the dtype that covers [rows, cols]."""
-    _dtype(t, dtype, name)
-    _layout(t, name)
-    _at_least(t, rows, cols, name)
+    """Row pitch of a 2-D row-major tensor of the dtype that covers [rows, cols]."""
+    if t.dtype is not dtype:
+        _dtype(t, dtype, name)
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or stride[1] != 1:
+        _layout(t, name)
+    if shape[0] < rows or shape[1] < cols:
+        _at_least(t, rows, cols, name)
+    return stride[0]
 
 
 def _vector(t, dtype, n, name):
-    _dtype(t, dtype, name)
+    if t.dtype is not dtype:
+        _dtype(t, dtype, name)
     if t.dim() != 1 or t.numel() < n or not t.is_contiguous():
         raise ValueError("%s must be a contiguous vector of at least %d entries" % (name, n))
 
@@ -603,11 +617,11 @@ def _gamma_kind(gamma, D):
     return _out_code(gamma.dtype)
 
 
-def _workspace(nbytes, device, stream):
+def _workspace(nbytes, like, stream):
     """Scratch of one call, allocated on the current stream; another stream
     that uses it is recorded, so that the memory is not handed out while that
     stream still runs."""
-    w = _torch().empty(nbytes, dtype=_torch().uint8, device=device)
+    w = _torch().empty(nbytes, dtype=_torch().uint8, device=like.device)
     if stream is not None and w.is_cuda:
         w.record_stream(stream)
     return w
@@ -620,35 +634,41 @@ def fp8_rmsnorm(x, gamma, eps=1e-6, residual=None, h=None, q=None, scales=None, 
     itself without a residual; y = h * rstd * gamma is quantised as
     fp8_quant_1x128 does it (from FP32, y is never stored). gamma [D] bf16 or
     float32. Returns (q uint8 [T, D], scales float32 [D/128, ld_s>=T], h,
-    rstd float32 [T]); h and rstd are what fp8_rmsnorm_bwd needs."""
+    rstd float32 [T]); h and rstd are what fp8_rmsnorm_bwd needs. h may be x
+    or residual (in place)."""
     torch = _torch()
-    bf16 = torch.bfloat16
-    _dtype(x, bf16, "x")
-    _layout(x, "x")
+    bf16, f32, u8 = torch.bfloat16, torch.float32, torch.uint8
+    ldx = _matrix(x, bf16, 0, 0, "x")
     T, D = x.shape
     kind = _gamma_kind(gamma, D)
-    dev = x.device
+    ldr = ldh = pr = ph = 0
     if residual is not None:
-        _dtype(residual, bf16, "residual")
-        _layout(residual, "residual")
+        ldr = _matrix(residual, bf16, T, D, "residual")
         if residual.shape != x.shape:
             raise ValueError("residual must be [%d, %d], got %s" % (T, D, tuple(residual.shape)))
-        h = torch.empty((T, D), dtype=bf16, device=dev) if h is None else h
-        _matrix(h, bf16, T, D, "h")
+        if h is None:
+            h = torch.empty((T, D), dtype=bf16, device=x.device)
+        ldh = _matrix(h, bf16, T, D, "h")
+        pr, ph = residual.data_ptr(), h.data_ptr()
     elif h is not None:
         raise ValueError("h is written only with a residual")
-    q = torch.empty((T, D), dtype=torch.uint8, device=dev) if q is None else q
-    scales = torch.empty((D // 128, _pad(max(T, 1), 4)), dtype=torch.float32, device=dev) if scales is None else scales
-    rstd = torch.empty(T, dtype=torch.float32, device=dev) if rstd is None else rstd
-    _quant_out(q, scales, (T, D), D // 128, T)
-    _vector(rstd, torch.float32, T, "rstd")
-    _on_gpu((x, "x"), (gamma, "gamma"), (residual, "residual"), (h, "h"), (q, "q"), (scales, "scales"), (rstd, "rstd"))
-    rc = lib().fp8_rmsnorm(x.data_ptr(), x.stride(0), None if residual is None else residual.data_ptr(),
-                           0 if residual is None else residual.stride(0), gamma.data_ptr(), kind, T, D, eps,
-                           None if h is None else h.data_ptr(), 0 if h is None else h.stride(0), q.data_ptr(),
-                           q.stride(0), scales.data_ptr(), scales.stride(0), rstd.data_ptr(), 1 if pow2 else 0,
-                           _stream(stream))
-    _check(rc, "fp8_rmsnorm")
+    if q is None:
+        q = torch.empty((T, D), dtype=u8, device=x.device)
+    if scales is None:
+        scales = torch.empty((D // 128, _pad(max(T, 1), 4)), dtype=f32, device=x.device)
+    if rstd is None:
+        rstd = torch.empty(T, dtype=f32, device=x.device)
+    ldq = _matrix(q, u8, T, D, "q")
+    lds = _matrix(scales, f32, D // 128, T, "scales")
+    _vector(rstd, f32, T, "rstd")
+    if not (x.is_cuda and gamma.is_cuda and q.is_cuda and scales.is_cuda and rstd.is_cuda
+            and (residual is None or (residual.is_cuda and h.is_cuda))):
+        _on_gpu((x, "x"), (gamma, "gamma"), (residual, "residual"), (h, "h"), (q, "q"), (scales, "scales"),
+                (rstd, "rstd"))
+    rc = lib().fp8_rmsnorm(x.data_ptr(), ldx, pr, ldr, gamma.data_ptr(), kind, T, D, eps, ph, ldh, q.data_ptr(), ldq,
+                           scales.data_ptr(), lds, rstd.data_ptr(), 1 if pow2 else 0, _stream(stream))
+    if rc:
+        _check(rc, "fp8_rmsnorm")
     return q, scales, x if h is None else h, rstd
 
 
@@ -657,19 +677,22 @@ def fp8_rmsnorm_t(h, rstd, gamma, qT=None, scalesT=None, stream=None, pow2=False
     fp8_quant_1x128(..., transpose=True) lays it out (T % 128 == 0): qT uint8
     [D, T], scalesT float32 [T/128, ld_s>=D]."""
     torch = _torch()
-    _dtype(h, torch.bfloat16, "h")
-    _layout(h, "h")
+    f32, u8 = torch.float32, torch.uint8
+    ldh = _matrix(h, torch.bfloat16, 0, 0, "h")
     T, D = h.shape
     kind = _gamma_kind(gamma, D)
-    _vector(rstd, torch.float32, T, "rstd")
-    qT = torch.empty((D, T), dtype=torch.uint8, device=h.device) if qT is None else qT
+    _vector(rstd, f32, T, "rstd")
+    if qT is None:
+        qT = torch.empty((D, T), dtype=u8, device=h.device)
     if scalesT is None:
-        scalesT = torch.empty((T // 128, _pad(max(D, 1), 4)), dtype=torch.float32, device=h.device)
-    _quant_out(qT, scalesT, (D, T), T // 128, D, "qT", "scalesT")
+        scalesT = torch.empty((T // 128, _pad(max(D, 1), 4)), dtype=f32, device=h.device)
+    ldq = _matrix(qT, u8, D, T, "qT")
+    lds = _matrix(scalesT, f32, T // 128, D, "scalesT")
     _on_gpu((h, "h"), (rstd, "rstd"), (gamma, "gamma"), (qT, "qT"), (scalesT, "scalesT"))
-    rc = lib().fp8_rmsnorm_t(h.data_ptr(), h.stride(0), rstd.data_ptr(), gamma.data_ptr(), kind, T, D, qT.data_ptr(),
-                             qT.stride(0), scalesT.data_ptr(), scalesT.stride(0), 1 if pow2 else 0, _stream(stream))
-    _check(rc, "fp8_rmsnorm_t")
+    rc = lib().fp8_rmsnorm_t(h.data_ptr(), ldh, rstd.data_ptr(), gamma.data_ptr(), kind, T, D, qT.data_ptr(), ldq,
+                             scalesT.data_ptr(), lds, 1 if pow2 else 0, _stream(stream))
+    if rc:
+        _check(rc, "fp8_rmsnorm_t")
     return qT, scalesT
 
 
@@ -677,28 +700,36 @@ def fp8_rmsnorm_bwd(dy, h, rstd, gamma, dres=None, dx=None, dgamma=None, stream=
     """Backward pass of fp8_rmsnorm: dy bf16 [T, D] is the gradient of its
     (dequantised) output, h and rstd what the forward call returned, dres the
     gradient that reaches h on the residual stream. Returns (dx bf16 [T, D],
-    dgamma float32 [D]); dx is the gradient of x and of the residual alike."""
+    dgamma float32 [D]); dx is the gradient of x and of the residual alike.
+    dx may be dy or dres (in place)."""
     torch = _torch()
-    bf16 = torch.bfloat16
-    _dtype(dy, bf16, "dy")
-    _layout(dy, "dy")
+    bf16, f32 = torch.bfloat16, torch.float32
+    lddy = _matrix(dy, bf16, 0, 0, "dy")
     T, D = dy.shape
-    _matrix(h, bf16, T, D, "h")
-    _vector(rstd, torch.float32, T, "rstd")
+    ldh = _matrix(h, bf16, T, D, "h")
+    _vector(rstd, f32, T, "rstd")
     kind = _gamma_kind(gamma, D)
+    lddres = pdres = 0
     if dres is not None:
-        _matrix(dres, bf16, T, D, "dres")
-    dx = torch.empty((T, D), dtype=bf16, device=dy.device) if dx is None else dx
-    dgamma = torch.empty(D, dtype=torch.float32, device=dy.device) if dgamma is None else dgamma
-    _matrix(dx, bf16, T, D, "dx")
-    _vector(dgamma, torch.float32, D, "dgamma")
-    _on_gpu((dy, "dy"), (h, "h"), (rstd, "rstd"), (gamma, "gamma"), (dres, "dres"), (dx, "dx"), (dgamma, "dgamma"))
-    ws = _workspace(lib().fp8_rmsnorm_bwd_workspace(T, D), dy.device, stream)
-    rc = lib().fp8_rmsnorm_bwd(dy.data_ptr(), dy.stride(0), h.data_ptr(), h.stride(0), rstd.data_ptr(),
-                               gamma.data_ptr(), kind, None if dres is None else dres.data_ptr(),
-                               0 if dres is None else dres.stride(0), T, D, dx.data_ptr(), dx.stride(0),
-                               dgamma.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
-    _check(rc, "fp8_rmsnorm_bwd")
+        lddres, pdres = _matrix(dres, bf16, T, D, "dres"), dres.data_ptr()
+    if dx is None:
+        dx = torch.empty((T, D), dtype=bf16, device=dy.device)
+    if dgamma is None:
+        dgamma = torch.empty(D, dtype=f32, device=dy.device)
+    lddx = _matrix(dx, bf16, T, D, "dx")
+    _vector(dgamma, f32, D, "dgamma")
+    if not (dy.is_cuda and h.is_cuda and rstd.is_cuda and gamma.is_cuda and dx.is_cuda and dgamma.is_cuda
+            and (dres is None or dres.is_cuda)):
+        _on_gpu((dy, "dy"), (h, "h"), (rstd, "rstd"), (gamma, "gamma"), (dres, "dres"), (dx, "dx"),
+                (dgamma, "dgamma"))
+    L = lib()
+    nbytes = L.fp8_rmsnorm_bwd_workspace(T, D)
+    ws = _workspace(nbytes, dy, stream)
+    rc = L.fp8_rmsnorm_bwd(dy.data_ptr(), lddy, h.data_ptr(), ldh, rstd.data_ptr(), gamma.data_ptr(), kind, pdres,
+                           lddres, T, D, dx.data_ptr(), lddx, dgamma.data_ptr(), ws.data_ptr(), nbytes,
+                           _stream(stream))
+    if rc:
+        _check(rc, "fp8_rmsnorm_bwd")
     return dx, dgamma
 
 
@@ -712,26 +743,37 @@ def fp8_gated_gemm(xq, sx, wq, sw, h=None, scales=None, gu=None, save=False, str
     gu the two projections in bf16 [M, 2I] for fp8_gated_bwd (None unless
     save=True or a gu buffer is given)."""
     torch = _torch()
-    M, N2, K = _gemm_operands(FPROP, xq, sx, wq, sw)
-    if N2 % 2:
-        raise ValueError("wq must stack as many up rows as gate rows, got %d rows" % N2)
+    f32, u8 = torch.float32, torch.uint8
+    ldx = _matrix(xq, u8, 0, 0, "xq")
+    M, K = xq.shape
+    ldsx = _matrix(sx, f32, K // 128, M, "sx")
+    ldw = _matrix(wq, u8, 0, 0, "wq")
+    N2 = wq.shape[0]
+    if wq.shape[1] != K or N2 % 2:
+        raise ValueError("wq must be [2I, K] with K = %d and as many up rows as gate rows, got %s"
+                         % (K, tuple(wq.shape)))
     I = N2 // 2
-    if not sw.is_contiguous() or tuple(sw.shape) != (N2 // 128, K // 128):
-        raise ValueError("sw must be a contiguous [%d, %d], got %s" % (N2 // 128, K // 128, tuple(sw.shape)))
-    dev = xq.device
-    h = torch.empty((M, I), dtype=torch.uint8, device=dev) if h is None else h
-    scales = torch.empty((I // 128, _pad(max(M, 1), 4)), dtype=torch.float32, device=dev) if scales is None else scales
+    if sw.dtype is not f32 or sw.shape != (N2 // 128, K // 128) or not sw.is_contiguous():
+        raise ValueError("sw must be a contiguous float32 [%d, %d], got %s %s"
+                         % (N2 // 128, K // 128, sw.dtype, tuple(sw.shape)))
+    if h is None:
+        h = torch.empty((M, I), dtype=u8, device=xq.device)
+    if scales is None:
+        scales = torch.empty((I // 128, _pad(max(M, 1), 4)), dtype=f32, device=xq.device)
     if gu is None and save:
-        gu = torch.empty((M, N2), dtype=torch.bfloat16, device=dev)
-    _quant_out(h, scales, (M, I), I // 128, M, "h", "scales")
+        gu = torch.empty((M, N2), dtype=torch.bfloat16, device=xq.device)
+    ldh = _matrix(h, u8, M, I, "h")
+    lds = _matrix(scales, f32, I // 128, M, "scales")
+    ldgu = pgu = 0
     if gu is not None:
-        _matrix(gu, torch.bfloat16, M, N2, "gu")
-    _on_gpu((xq, "xq"), (sx, "sx"), (wq, "wq"), (sw, "sw"), (h, "h"), (scales, "scales"), (gu, "gu"))
-    rc = lib().fp8_gated_gemm(xq.data_ptr(), sx.data_ptr(), xq.stride(0), sx.stride(0), wq.data_ptr(), sw.data_ptr(),
-                              wq.stride(0), M, I, K, h.data_ptr(), h.stride(0), scales.data_ptr(), scales.stride(0),
-                              None if gu is None else gu.data_ptr(), 0 if gu is None else gu.stride(0),
-                              1 if pow2 else 0, _stream(stream))
-    _check(rc, "fp8_gated_gemm")
+        ldgu, pgu = _matrix(gu, torch.bfloat16, M, N2, "gu"), gu.data_ptr()
+    if not (xq.is_cuda and sx.is_cuda and wq.is_cuda and sw.is_cuda and h.is_cuda and scales.is_cuda
+            and (gu is None or gu.is_cuda)):
+        _on_gpu((xq, "xq"), (sx, "sx"), (wq, "wq"), (sw, "sw"), (h, "h"), (scales, "scales"), (gu, "gu"))
+    rc = lib().fp8_gated_gemm(xq.data_ptr(), sx.data_ptr(), ldx, ldsx, wq.data_ptr(), sw.data_ptr(), ldw, M, I, K,
+                              h.data_ptr(), ldh, scales.data_ptr(), lds, pgu, ldgu, 1 if pow2 else 0, _stream(stream))
+    if rc:
+        _check(rc, "fp8_gated_gemm")
     return h, scales, gu
 
 
@@ -744,31 +786,37 @@ def fp8_gated_bwd(gu, dh, q=None, scales=None, qT=None, scalesT=None, hqT=None, 
     recomputed h per column (hqT [I, M], hscalesT [M/128, >=I]: the down
     projection's wgrad operand)."""
     torch = _torch()
-    u8, f32 = torch.uint8, torch.float32
-    _dtype(gu, torch.bfloat16, "gu")
-    _dtype(dh, torch.bfloat16, "dh")
-    _layout(gu, "gu")
-    _layout(dh, "dh")
+    u8, f32, bf16 = torch.uint8, torch.float32, torch.bfloat16
+    ldgu = _matrix(gu, bf16, 0, 0, "gu")
+    lddh = _matrix(dh, bf16, 0, 0, "dh")
     M, I = dh.shape
-    if tuple(gu.shape) != (M, 2 * I):
+    if gu.shape != (M, 2 * I):
         raise ValueError("gu must be [%d, %d], got %s" % (M, 2 * I, tuple(gu.shape)))
     dev = dh.device
-    q = torch.empty((M, 2 * I), dtype=u8, device=dev) if q is None else q
-    scales = torch.empty((2 * I // 128, _pad(max(M, 1), 4)), dtype=f32, device=dev) if scales is None else scales
-    qT = torch.empty((2 * I, M), dtype=u8, device=dev) if qT is None else qT
-    scalesT = torch.empty((M // 128, _pad(max(2 * I, 1), 4)), dtype=f32, device=dev) if scalesT is None else scalesT
-    hqT = torch.empty((I, M), dtype=u8, device=dev) if hqT is None else hqT
-    hscalesT = torch.empty((M // 128, _pad(max(I, 1), 4)), dtype=f32, device=dev) if hscalesT is None else hscalesT
-    _quant_out(q, scales, (M, 2 * I), 2 * I // 128, M)
-    _quant_out(qT, scalesT, (2 * I, M), M // 128, 2 * I, "qT", "scalesT")
-    _quant_out(hqT, hscalesT, (I, M), M // 128, I, "hqT", "hscalesT")
-    _on_gpu((gu, "gu"), (dh, "dh"), (q, "q"), (scales, "scales"), (qT, "qT"), (scalesT, "scalesT"), (hqT, "hqT"),
-            (hscalesT, "hscalesT"))
-    rc = lib().fp8_gated_bwd(gu.data_ptr(), gu.stride(0), dh.data_ptr(), dh.stride(0), M, I, q.data_ptr(), q.stride(0),
-                             scales.data_ptr(), scales.stride(0), qT.data_ptr(), qT.stride(0), scalesT.data_ptr(),
-                             scalesT.stride(0), hqT.data_ptr(), hqT.stride(0), hscalesT.data_ptr(),
-                             hscalesT.stride(0), 1 if pow2 else 0, _stream(stream))
-    _check(rc, "fp8_gated_bwd")
+    if q is None:
+        q = torch.empty((M, 2 * I), dtype=u8, device=dev)
+    if scales is None:
+        scales = torch.empty((2 * I // 128, _pad(max(M, 1), 4)), dtype=f32, device=dev)
+    if qT is None:
+        qT = torch.empty((2 * I, M), dtype=u8, device=dev)
+    if scalesT is None:
+        scalesT = torch.empty((M // 128, _pad(max(2 * I, 1), 4)), dtype=f32, device=dev)
+    if hqT is None:
+        hqT = torch.empty((I, M), dtype=u8, device=dev)
+    if hscalesT is None:
+        hscalesT = torch.empty((M // 128, _pad(max(I, 1), 4)), dtype=f32, device=dev)
+    ldq, lds = _matrix(q, u8, M, 2 * I, "q"), _matrix(scales, f32, 2 * I // 128, M, "scales")
+    ldqT, ldsT = _matrix(qT, u8, 2 * I, M, "qT"), _matrix(scalesT, f32, M // 128, 2 * I, "scalesT")
+    ldhT, ldhs = _matrix(hqT, u8, I, M, "hqT"), _matrix(hscalesT, f32, M // 128, I, "hscalesT")
+    if not (gu.is_cuda and dh.is_cuda and q.is_cuda and scales.is_cuda and qT.is_cuda and scalesT.is_cuda
+            and hqT.is_cuda and hscalesT.is_cuda):
+        _on_gpu((gu, "gu"), (dh, "dh"), (q, "q"), (scales, "scales"), (qT, "qT"), (scalesT, "scalesT"), (hqT, "hqT"),
+                (hscalesT, "hscalesT"))
+    rc = lib().fp8_gated_bwd(gu.data_ptr(), ldgu, dh.data_ptr(), lddh, M, I, q.data_ptr(), ldq, scales.data_ptr(), lds,
+                             qT.data_ptr(), ldqT, scalesT.data_ptr(), ldsT, hqT.data_ptr(), ldhT, hscalesT.data_ptr(),
+                             ldhs, 1 if pow2 else 0, _stream(stream))
+    if rc:
+        _check(rc, "fp8_gated_bwd")
     return q, scales, qT, scalesT, hqT, hscalesT
 
 
@@ -776,40 +824,51 @@ def grad_clip(grads, max_norm, eps=1e-6, out=None, norm=None, stream=None):
     """Scale gradients so that their global L2 norm is at most max_norm.
 
     grads: contiguous float32 or bfloat16 CUDA tensors of any shape (views into
-    a bucket included). out: tensors to write, of the same shapes and types
+    a bucket included). out: tensors to write, of the same sizes and types
     (default: the gradients themselves). Returns (norm, out): norm float32 [2]
     on the device holds the norm before scaling and the factor min(1, max_norm
     / (norm + eps)); nothing is copied to the host."""
     torch = _torch()
-    f32, bf16 = torch.float32, torch.bfloat16
     grads = list(grads)
     outs = grads if out is None else list(out)
-    if len(outs) != len(grads):
+    n = len(grads)
+    if len(outs) != n:
         raise ValueError("out must hold one tensor per gradient")
-    if not grads:
+    if not n:
         raise ValueError("grads must hold at least one tensor")
-    rows = []
-    for g, o in zip(grads, outs):
-        dt = g.dtype
-        if dt is not f32 and dt is not bf16:
-            raise ValueError("gradients must be float32 or bfloat16, got %s" % dt)
-        n = g.numel()
-        if not g.is_contiguous():
-            raise ValueError("gradients must be contiguous")
-        if o is not g and (o.dtype is not dt or o.numel() != n or not o.is_contiguous()):
-            raise ValueError("out must match the gradients' shapes and types and be contiguous")
-        if not (g.is_cuda and o.is_cuda):
-            raise ValueError("grads and out must be CUDA tensors")
-        rows += (g.data_ptr(), o.data_ptr(), n, OUT_F32 if dt is f32 else OUT_BF16)
-    dev = grads[0].device
-    norm = torch.empty(2, dtype=f32, device=dev) if norm is None else norm
-    _vector(norm, f32, 2, "norm")
-    _on_gpu((norm, "norm"))
-    table = (ctypes.c_int64 * len(rows))(*rows)
-    ws = _workspace(lib().fp8fg_grad_clip_workspace(len(grads)), dev, stream)
-    rc = lib().fp8fg_grad_clip(table, len(grads), max_norm, eps, norm.data_ptr(), ws.data_ptr(), ws.numel(),
-                               _stream(stream))
-    _check(rc, "fp8fg_grad_clip")
+    # one pass of C-level calls per attribute: with hundreds of tensors the
+    # lists are the cost of the call
+    Tensor = torch.Tensor
+    kind_of = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
+    types, sizes = list(map(attrgetter("dtype"), grads)), list(map(Tensor.numel, grads))
+    if not all(map(kind_of.__contains__, types)):
+        raise ValueError("gradients must be float32 or bfloat16")
+    if not all(map(Tensor.is_contiguous, grads)):
+        raise ValueError("gradients must be contiguous")
+    ptrs = array("q", map(Tensor.data_ptr, grads))
+    if out is None:
+        out_ptrs = ptrs
+    else:
+        if list(map(attrgetter("dtype"), outs)) != types or list(map(Tensor.numel, outs)) != sizes \
+                or not all(map(Tensor.is_contiguous, outs)):
+            raise ValueError("out must match the gradients' sizes and types and be contiguous")
+        out_ptrs = array("q", map(Tensor.data_ptr, outs))
+    if norm is None:
+        norm = torch.empty(2, dtype=torch.float32, device=grads[0].device)
+    _vector(norm, torch.float32, 2, "norm")
+    is_cuda = attrgetter("is_cuda")
+    if not (norm.is_cuda and all(map(is_cuda, grads)) and (out is None or all(map(is_cuda, outs)))):
+        raise ValueError("grads, out and norm must be CUDA tensors")
+    table = array("q", bytes(32 * n))       # fp8fg_grad: g, out, n, kind (with its padding)
+    table[0::4], table[1::4], table[2::4] = ptrs, out_ptrs, array("q", sizes)
+    table[3::4] = array("q", map(kind_of.__getitem__, types))
+    L = lib()
+    nbytes = L.fp8fg_grad_clip_workspace(n)
+    ws = _workspace(nbytes, norm, stream)
+    rc = L.fp8fg_grad_clip(table.buffer_info()[0], n, max_norm, eps, norm.data_ptr(), ws.data_ptr(), nbytes,
+                           _stream(stream))
+    if rc:
+        _check(rc, "fp8fg_grad_clip")
     return norm, outs
 
 

@@ -181,11 +181,11 @@ def test_binding_gated():
     M, K, I = 5, 256, 128
     xq, sx, wq, sw = z((M, K), U8), z((2, 8), F32), z((2 * I, K), U8), z((2, 2), F32)
     expect("CUDA tensor", fg.fp8_gated_gemm, xq, sx, wq, sw)
-    expect("K = a.shape", fg.fp8_gated_gemm, xq, sx, wq[:, :128], sw)
+    expect("K = 256", fg.fp8_gated_gemm, xq, sx, wq[:, :128], sw)
     expect("up rows", fg.fp8_gated_gemm, xq, sx, z((129, K), U8), sw)
     expect("sw must be", fg.fp8_gated_gemm, xq, sx, wq, z((2, 4), F32)[:, :2])
     expect("sw must be", fg.fp8_gated_gemm, xq, sx, wq, z((3, 2), F32))
-    expect("sa must cover", fg.fp8_gated_gemm, xq, sx[:, :4], wq, sw)
+    expect("sx must cover", fg.fp8_gated_gemm, xq, sx[:, :4], wq, sw)
     expect("h must cover", fg.fp8_gated_gemm, xq, sx, wq, sw, h=z((M, 64), U8))
     expect("scales must cover", fg.fp8_gated_gemm, xq, sx, wq, sw, scales=z((1, 4), F32))
     expect("gu must cover", fg.fp8_gated_gemm, xq, sx, wq, sw, gu=z((M, I), BF16))
