@@ -15,9 +15,13 @@
 //   dx[j]    = rstd * (a[j] - h[j] * rstd * c) (+ dres[j])
 //   dgamma[j] = sum_t dy[t][j] * h[t][j] * rstd[t]
 //
-// All three are streams of whole rows: the row's chunks of 8 columns (16
-// bytes) stay in registers from the load to the last store, so each tensor
-// crosses the memory once.
+// Forward and backward are streams of whole rows. A row has to be reduced
+// before its first output is known, so a CTA that loads, reduces and stores one
+// row after the other leaves the memory idle most of the time. Each CTA
+// therefore has its next rows brought into a ring in shared memory by bulk
+// copies (about 170 KB in flight per SM, whatever the row's width) while it
+// works on the current one; the row's values stay in registers from there to
+// the last store, so each tensor crosses the memory once.
 #include <cuda_bf16.h>
 
 #include "group_rule.cuh"
@@ -30,8 +34,13 @@ namespace {
 constexpr int GROUP = 128;
 constexpr int64_t NORM_MAX_D = 18432;  // 768 threads x 3 chunks of 8 columns
 
-// largest CTA of a kernel whose threads own CPT chunks of a row (row_shape)
-constexpr int max_threads(int cpt) { return 256 * cpt; }
+// Widths of a kernel: chunks of 8 columns per thread, the largest CTA and the
+// CTAs of that size per SM that the registers must allow. Rows of up to 1024
+// columns take one warp; WIDE starts above 8192 columns.
+enum Width { ONE = 0, TWO = 1, FOUR = 2, WIDE = 3 };
+constexpr int cpt_of(int w) { return w == ONE ? 1 : (w == TWO ? 2 : (w == FOUR ? 4 : 3)); }
+constexpr int max_threads(int w) { return w < FOUR ? 32 : (w == FOUR ? 256 : 768); }
+constexpr int min_ctas(int w, bool bwd) { return w < FOUR ? (bwd ? 12 : 28) : (w == FOUR ? (bwd ? 2 : 3) : 1); }
 
 // (not the read-only path: the outputs may be the inputs' own buffers)
 __device__ __forceinline__ uint4 ld_stream(const uint16_t *p)
@@ -43,40 +52,49 @@ __device__ __forceinline__ uint4 ld_stream(const uint16_t *p)
     return v;
 }
 
-__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8])
+// 8 bf16 values <-> 4 pairs of FP32 (the arithmetic below is on pairs: one
+// instruction for two elements)
+__device__ __forceinline__ void unpack8(const uint4 &v, float2 (&f)[4])
 {
-    f[0] = bf16_lo(v.x);
-    f[1] = bf16_hi(v.x);
-    f[2] = bf16_lo(v.y);
-    f[3] = bf16_hi(v.y);
-    f[4] = bf16_lo(v.z);
-    f[5] = bf16_hi(v.z);
-    f[6] = bf16_lo(v.w);
-    f[7] = bf16_hi(v.w);
+    f[0] = make_float2(bf16_lo(v.x), bf16_hi(v.x));
+    f[1] = make_float2(bf16_lo(v.y), bf16_hi(v.y));
+    f[2] = make_float2(bf16_lo(v.z), bf16_hi(v.z));
+    f[3] = make_float2(bf16_lo(v.w), bf16_hi(v.w));
 }
 
-__device__ __forceinline__ uint32_t pack2(float a, float b)
+__device__ __forceinline__ uint32_t pack2(float2 a)
 {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    const __nv_bfloat162 h = __float22bfloat162_rn(a);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&f)[8])
+__device__ __forceinline__ uint4 pack8(const float2 (&f)[4])
 {
-    return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+    return make_uint4(pack2(f[0]), pack2(f[1]), pack2(f[2]), pack2(f[3]));
 }
 
-// the norm's weight at columns 8c .. 8c+7
-__device__ __forceinline__ void load_gamma(const void *gamma, bool f32, int c, float (&g)[8])
+// bf16(a + b) of two pairs: one exact sum, one rounding
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b)
+{
+    const __nv_bfloat162 s = __hadd2_rn(*reinterpret_cast<const __nv_bfloat162 *>(&a),
+                                        *reinterpret_cast<const __nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&s);
+}
+
+// the norm's weight at columns 8c .. 8c+7 (global or shared memory)
+__device__ __forceinline__ void load_gamma(const void *gamma, bool f32, int c, float2 (&g)[4])
 {
     if (f32) {
-        const float4 a = __ldg(static_cast<const float4 *>(gamma) + 2 * c);
-        const float4 b = __ldg(static_cast<const float4 *>(gamma) + 2 * c + 1);
-        g[0] = a.x, g[1] = a.y, g[2] = a.z, g[3] = a.w, g[4] = b.x, g[5] = b.y, g[6] = b.z, g[7] = b.w;
+        const float4 a = static_cast<const float4 *>(gamma)[2 * c];
+        const float4 b = static_cast<const float4 *>(gamma)[2 * c + 1];
+        g[0] = make_float2(a.x, a.y), g[1] = make_float2(a.z, a.w);
+        g[2] = make_float2(b.x, b.y), g[3] = make_float2(b.z, b.w);
     } else {
-        unpack8(__ldg(static_cast<const uint4 *>(gamma) + c), g);
+        unpack8(static_cast<const uint4 *>(gamma)[c], g);
     }
 }
+
+__device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
 
 // Sum over the block in a fixed order. `part` holds one slot per warp and is
 // rewritten by the next call, so calls alternate between two of them: a
@@ -87,8 +105,10 @@ __device__ __forceinline__ float block_sum(float v, float *part, int nwarps)
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1)
         v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (nwarps == 1)
+    if (nwarps == 1) {
+        __syncwarp();
         return v;
+    }
     if ((threadIdx.x & 31) == 0)
         part[threadIdx.x >> 5] = v;
     __syncthreads();
@@ -97,6 +117,49 @@ __device__ __forceinline__ float block_sum(float v, float *part, int nwarps)
     for (int o = 16; o >= 1; o >>= 1)
         v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
+}
+
+// Dynamic shared memory: the ring, `slots` slots of `tensors` rows of D bf16
+// values each; one "row landed" barrier per slot; gamma (backward). Rows are the
+// CTA's own: blockIdx, blockIdx + grid, ...
+constexpr int MAX_SLOTS = 8;
+constexpr uint32_t BAR_BYTES = 8 * MAX_SLOTS;
+
+struct Ring {
+    uint32_t base, bars, slot_bytes;
+    int slots;
+    // of the row being worked on
+    int slot = 0;
+    uint32_t phase = 0;
+
+    __device__ __forceinline__ void next()
+    {
+        if (++slot == slots) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+    __device__ __forceinline__ uint32_t bar() const { return bars + 8 * slot; }
+};
+
+__device__ __forceinline__ uint4 lds16(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+
+// A wait that ran out (FP8FG_ETIMEOUT is recorded) does not leave the loop,
+// whose barriers need every thread: the CTA's remaining rows are worked on
+// with whatever the ring holds, no further copy is issued, and before the CTA
+// exits thread 0 waits (bounded) for those in flight.
+__device__ __forceinline__ void drain(const Ring &ring, uint32_t pending, uint32_t parity, uint64_t limit_ns)
+{
+    const uint64_t t0 = global_timer_ns();
+    for (int s = 0; s < ring.slots; ++s)
+        while (((pending >> s) & 1u) && !mbar_try_wait(ring.bars + 8 * s, (parity >> s) & 1u) &&
+               global_timer_ns() - t0 < limit_ns) {
+        }
 }
 
 struct NormFwd {
@@ -109,83 +172,127 @@ struct NormFwd {
     int D;
     float eps;
     bool gamma_f32;
+    int slots;
+    int *status;
+    uint64_t wait_limit_ns;
 };
 
 // One row per CTA at a time: thread t owns chunks t, t + blockDim, ...; a
 // half-warp's 16 chunks are one 128-column group (D % 128 == 0 and blockDim
 // % 32 == 0 keep every group inside one half-warp).
-template <int CPT, bool RES, bool P2>
-__global__ void __launch_bounds__(max_threads(CPT)) rmsnorm_fwd_kernel(const NormFwd p)
+template <int W, bool RES, bool P2>
+__global__ void __launch_bounds__(max_threads(W), min_ctas(W, false)) rmsnorm_fwd_kernel(const NormFwd p)
 {
-    griddep_launch_dependents();
-    griddep_wait();
+    extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float part[2][32];
+    __shared__ int abort_flag;
+    constexpr int TENSORS = RES ? 2 : 1, CPT = cpt_of(W);
     const int nchunk = p.D / 8, nwarps = blockDim.x >> 5;
+    const uint32_t row_bytes = 2 * (uint32_t)p.D;
+    Ring ring{smem_u32(smem), smem_u32(smem) + p.slots * TENSORS * row_bytes, TENSORS * row_bytes, p.slots};
+    const WaitCtl wc{&abort_flag, p.status, p.wait_limit_ns};
+    uint32_t pending = 0, parity = 0;  // thread 0: slots ever filled, parity of the last fill
+    auto fetch = [&](int64_t t, int slot, uint32_t par) {
+        const uint32_t bar = ring.bars + 8 * slot, dst = ring.base + slot * ring.slot_bytes;
+        mbar_arrive_expect_tx(bar, ring.slot_bytes);
+        bulk_load(dst, p.x + t * p.ldx, row_bytes, bar);
+        if constexpr (RES)
+            bulk_load(dst + row_bytes, p.r + t * p.ldr, row_bytes, bar);
+        pending |= 1u << slot;
+        parity = (parity & ~(1u << slot)) | (par << slot);
+    };
+    griddep_launch_dependents();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.slots; ++s)
+            mbar_init(ring.bars + 8 * s, 1);
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    griddep_wait();
+    if (threadIdx.x == 0)
+        for (int s = 0; s < p.slots && blockIdx.x + (int64_t)s * gridDim.x < p.T; ++s)
+            fetch(blockIdx.x + (int64_t)s * gridDim.x, s, 0);
+    __syncthreads();
     int b = 0;
-    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, b ^= 1) {
-        uint4 v[CPT], rv[CPT];
+    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, b ^= 1, ring.next()) {
+        mbar_wait(ring.bar(), ring.phase, wc, FP8FG_ETIMEOUT);
+        const uint32_t src = ring.base + ring.slot * ring.slot_bytes;
+        uint4 v[CPT];
+        float2 ss2 = splat(0.0f);
 #pragma unroll
         for (int i = 0; i < CPT; ++i) {
             const int c = threadIdx.x + i * blockDim.x;
-            v[i] = rv[i] = make_uint4(0, 0, 0, 0);
+            v[i] = make_uint4(0, 0, 0, 0);
             if (c < nchunk) {
-                v[i] = ld_stream(p.x + t * p.ldx + 8 * c);
-                if constexpr (RES)
-                    rv[i] = ld_stream(p.r + t * p.ldr + 8 * c);
-            }
-        }
-        float ss = 0.0f;
-#pragma unroll
-        for (int i = 0; i < CPT; ++i) {
-            float f[8];
-            unpack8(v[i], f);
-            if constexpr (RES) {
-                float r[8];
-                unpack8(rv[i], r);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    f[e] += r[e];
-                v[i] = pack8(f);
-                unpack8(v[i], f);  // the rounded sum
-                const int c = threadIdx.x + i * blockDim.x;
-                if (c < nchunk)
+                v[i] = lds16(src + 16 * c);
+                if constexpr (RES) {
+                    const uint4 r = lds16(src + row_bytes + 16 * c);
+                    v[i] = make_uint4(add_bf16x2(v[i].x, r.x), add_bf16x2(v[i].y, r.y), add_bf16x2(v[i].z, r.z),
+                                      add_bf16x2(v[i].w, r.w));
                     *reinterpret_cast<uint4 *>(p.h + t * p.ldh + 8 * c) = v[i];
+                }
             }
+            float2 f[4];
+            unpack8(v[i], f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                ss = fmaf(f[e], f[e], ss);
+            for (int e = 0; e < 4; ++e)
+                ss2 = __ffma2_rn(f[e], f[e], ss2);
         }
-        ss = block_sum(ss, part[b], nwarps);
+        const float ss = block_sum(ss2.x + ss2.y, part[b], nwarps);
+        // (the sum's barrier: every thread has read the slot)
+        if (threadIdx.x == 0) {
+            const int64_t ahead = t + (int64_t)p.slots * gridDim.x;
+            if (ahead < p.T && !*wc.abort_flag)
+                fetch(ahead, ring.slot, ring.phase ^ 1);
+        }
         const float rstd = rsqrtf(ss / (float)p.D + p.eps);
         if (threadIdx.x == 0)
             p.rstd[t] = rstd;
+        // the groups' maxima, then one division sequence for a half-warp's CPT
+        // groups: lane i of it takes the group of chunk i
+        const float2 rstd2 = splat(rstd);
+        float2 y[CPT][4];
+        float mine = 0.0f;
 #pragma unroll
         for (int i = 0; i < CPT; ++i) {
             const int c = threadIdx.x + i * blockDim.x;
-            const bool live = c < nchunk;
-            float f[8], g[8];
-            unpack8(v[i], f);
-            load_gamma(p.gamma, p.gamma_f32, live ? c : 0, g);
+            float2 g[4];
+            unpack8(v[i], y[i]);
+            load_gamma(p.gamma, p.gamma_f32, c < nchunk ? c : 0, g);
             float amax = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                f[e] = f[e] * rstd * g[e];
-                amax = fmaxf(amax, fabsf(f[e]));
+            for (int e = 0; e < 4; ++e) {
+                y[i][e] = __fmul2_rn(__fmul2_rn(y[i][e], rstd2), g[e]);
+                amax = fmaxf(amax, fmaxf(fabsf(y[i][e].x), fabsf(y[i][e].y)));
             }
 #pragma unroll
             for (int o = 8; o >= 1; o >>= 1)
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            const ScalePair sp = group_scale_rule<P2>(amax);
-            if (live) {
+            mine = (int)(threadIdx.x & 15) == i ? amax : mine;
+        }
+        const ScalePair sp = group_scale_rule<P2>(mine);
+        if ((threadIdx.x & 15) < CPT) {
+            const int c = (threadIdx.x & ~15) + (threadIdx.x & 15) * blockDim.x;
+            if (c < nchunk)
+                p.scales[(int64_t)(c >> 4) * p.ld_s + t] = sp.s;
+        }
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) {
+            const int c = threadIdx.x + i * blockDim.x;
+            const float2 inv = splat(__shfl_sync(0xffffffffu, sp.inv, (threadIdx.x & 16) + i));
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                y[i][e] = __fmul2_rn(y[i][e], inv);
+            if (c < nchunk) {
                 uint2 o;
-                o.x = cvt_e4m3x2(f[0] * sp.inv, f[1] * sp.inv) | (cvt_e4m3x2(f[2] * sp.inv, f[3] * sp.inv) << 16);
-                o.y = cvt_e4m3x2(f[4] * sp.inv, f[5] * sp.inv) | (cvt_e4m3x2(f[6] * sp.inv, f[7] * sp.inv) << 16);
+                o.x = cvt_e4m3x2(y[i][0].x, y[i][0].y) | (cvt_e4m3x2(y[i][1].x, y[i][1].y) << 16);
+                o.y = cvt_e4m3x2(y[i][2].x, y[i][2].y) | (cvt_e4m3x2(y[i][3].x, y[i][3].y) << 16);
                 *reinterpret_cast<uint2 *>(p.q + t * p.ldq + 8 * c) = o;
-                if ((c & 15) == 0)
-                    p.scales[(int64_t)(c >> 4) * p.ld_s + t] = sp.s;
             }
         }
     }
+    if (threadIdx.x == 0 && *wc.abort_flag)
+        drain(ring, pending, parity, p.wait_limit_ns);
 }
 
 // y^T in groups of 128 rows: CTA tile 128 rows x 64 columns. Thread (c, part)
@@ -251,158 +358,260 @@ struct NormBwd {
     int64_t T, lddy, ldh, lddres, lddx;
     int D;
     bool gamma_f32;
+    int slots;
+    int *status;
+    uint64_t wait_limit_ns;
 };
 
-// Rows blockIdx, blockIdx + grid, ...; the thread's columns are the same in
-// every row, so its dgamma terms add up in registers and leave once, as the
-// CTA's row of `part`. norm_dgamma_kernel adds those rows up in order, so the
-// result does not depend on the schedule.
-template <int CPT, bool RES>
-__global__ void __launch_bounds__(max_threads(CPT)) rmsnorm_bwd_kernel(const NormBwd p)
+// The thread's columns are the same in every row, so its dgamma terms add up
+// in registers and leave once, as the CTA's row of `part`.
+// norm_dgamma_kernel adds those rows up in order, so the result does not
+// depend on the schedule. The row's values go from the ring to registers as
+// they are (bf16), so that the slot can be refilled under the second half of
+// the row's work: with two slots a CTA then always has two rows in flight
+// (8192 x 7168 with dres 75.9 us; 87 when the row was read from the ring
+// twice and held its slot).
+template <int W, bool RES>
+__global__ void __launch_bounds__(max_threads(W), min_ctas(W, true)) rmsnorm_bwd_kernel(const NormBwd p)
 {
-    griddep_launch_dependents();
-    griddep_wait();
+    extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float sums[2][32];
+    __shared__ int abort_flag;
+    constexpr int TENSORS = RES ? 3 : 2, CPT = cpt_of(W);
     const int nchunk = p.D / 8, nwarps = blockDim.x >> 5;
-    float dg[CPT][8];
+    const uint32_t row_bytes = 2 * (uint32_t)p.D;
+    Ring ring{smem_u32(smem), smem_u32(smem) + p.slots * TENSORS * row_bytes, TENSORS * row_bytes, p.slots};
+    uint8_t *const staged = smem + p.slots * TENSORS * row_bytes + BAR_BYTES;
+    const void *const gamma = W == WIDE ? p.gamma : staged;
+    const WaitCtl wc{&abort_flag, p.status, p.wait_limit_ns};
+    uint32_t pending = 0, parity = 0;
+    auto fetch = [&](int64_t t, int slot, uint32_t par) {
+        const uint32_t bar = ring.bars + 8 * slot, dst = ring.base + slot * ring.slot_bytes;
+        mbar_arrive_expect_tx(bar, ring.slot_bytes);
+        bulk_load(dst, p.dy + t * p.lddy, row_bytes, bar);
+        bulk_load(dst + row_bytes, p.h + t * p.ldh, row_bytes, bar);
+        if constexpr (RES)
+            bulk_load(dst + 2 * row_bytes, p.dres + t * p.lddres, row_bytes, bar);
+        pending |= 1u << slot;
+        parity = (parity & ~(1u << slot)) | (par << slot);
+    };
+    griddep_launch_dependents();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.slots; ++s)
+            mbar_init(ring.bars + 8 * s, 1);
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    griddep_wait();
+    if (threadIdx.x == 0)
+        for (int s = 0; s < p.slots && blockIdx.x + (int64_t)s * gridDim.x < p.T; ++s)
+            fetch(blockIdx.x + (int64_t)s * gridDim.x, s, 0);
+    // gamma is read twice per row: from global memory each row would wait for
+    // it again. (The widest rows need the space for their second slot.)
+    if constexpr (W != WIDE)
+        for (int i = threadIdx.x; i < (p.gamma_f32 ? p.D / 4 : p.D / 8); i += blockDim.x)
+            reinterpret_cast<uint4 *>(staged)[i] = static_cast<const uint4 *>(p.gamma)[i];
+    __syncthreads();
+    float2 dg[CPT][4];
 #pragma unroll
     for (int i = 0; i < CPT; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            dg[i][e] = 0.0f;
+        for (int e = 0; e < 4; ++e)
+            dg[i][e] = splat(0.0f);
     int b = 0;
-    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, b ^= 1) {
+    float rstd = blockIdx.x < p.T ? __ldg(p.rstd + blockIdx.x) : 0.0f;
+    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, b ^= 1, ring.next()) {
+        const float rstd_next = t + gridDim.x < p.T ? __ldg(p.rstd + t + gridDim.x) : 0.0f;
+        mbar_wait(ring.bar(), ring.phase, wc, FP8FG_ETIMEOUT);
+        const uint32_t src = ring.base + ring.slot * ring.slot_bytes;
         uint4 dv[CPT], hv[CPT], rv[CPT];
-        const float rstd = __ldg(p.rstd + t);
+        float2 dot2 = splat(0.0f);
 #pragma unroll
         for (int i = 0; i < CPT; ++i) {
             const int c = threadIdx.x + i * blockDim.x;
-            dv[i] = hv[i] = rv[i] = make_uint4(0, 0, 0, 0);
             if (c < nchunk) {
-                dv[i] = ld_stream(p.dy + t * p.lddy + 8 * c);
-                hv[i] = ld_stream(p.h + t * p.ldh + 8 * c);
+                dv[i] = lds16(src + 16 * c);
+                hv[i] = lds16(src + row_bytes + 16 * c);
                 if constexpr (RES)
-                    rv[i] = ld_stream(p.dres + t * p.lddres + 8 * c);
+                    rv[i] = lds16(src + 2 * row_bytes + 16 * c);
+                float2 d[4], h[4], g[4];
+                unpack8(dv[i], d);
+                unpack8(hv[i], h);
+                load_gamma(gamma, p.gamma_f32, c, g);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 dh = __fmul2_rn(d[e], h[e]);
+                    dg[i][e] = __ffma2_rn(dh, splat(rstd), dg[i][e]);
+                    dot2 = __ffma2_rn(dh, g[e], dot2);
+                }
             }
         }
-        float dot = 0.0f;
-#pragma unroll
-        for (int i = 0; i < CPT; ++i) {
-            const int c = threadIdx.x + i * blockDim.x;
-            float d[8], h[8], g[8];
-            unpack8(dv[i], d);
-            unpack8(hv[i], h);
-            load_gamma(p.gamma, p.gamma_f32, c < nchunk ? c : 0, g);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float dh = d[e] * h[e];
-                dg[i][e] = fmaf(dh, rstd, dg[i][e]);
-                dot = fmaf(dh, g[e], dot);
-            }
+        const float dot = block_sum(dot2.x + dot2.y, sums[b], nwarps);
+        // (the sum's barrier: every thread has read the slot)
+        if (threadIdx.x == 0) {
+            const int64_t ahead = t + (int64_t)p.slots * gridDim.x;
+            if (ahead < p.T && !*wc.abort_flag)
+                fetch(ahead, ring.slot, ring.phase ^ 1);
         }
-        dot = block_sum(dot, sums[b], nwarps);
         const float k = dot / (float)p.D * rstd * rstd;  // dx = rstd * (a - h k)
 #pragma unroll
         for (int i = 0; i < CPT; ++i) {
             const int c = threadIdx.x + i * blockDim.x;
             if (c >= nchunk)
                 continue;
-            float d[8], h[8], g[8], r[8];
+            float2 d[4], h[4], g[4];
             unpack8(dv[i], d);
             unpack8(hv[i], h);
-            unpack8(rv[i], r);
-            load_gamma(p.gamma, p.gamma_f32, c, g);
+            load_gamma(gamma, p.gamma_f32, c, g);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float v = rstd * fmaf(-h[e], k, d[e] * g[e]);
-                d[e] = RES ? v + r[e] : v;
+            for (int e = 0; e < 4; ++e)
+                d[e] = __ffma2_rn(h[e], splat(-k), __fmul2_rn(d[e], g[e]));
+            if constexpr (RES) {
+                unpack8(rv[i], h);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    d[e] = __ffma2_rn(d[e], splat(rstd), h[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    d[e] = __fmul2_rn(d[e], splat(rstd));
             }
             *reinterpret_cast<uint4 *>(p.dx + t * p.lddx + 8 * c) = pack8(d);
         }
+        rstd = rstd_next;
     }
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
         const int c = threadIdx.x + i * blockDim.x;
         if (c < nchunk) {
             float4 *o = reinterpret_cast<float4 *>(p.part + (int64_t)blockIdx.x * p.D + 8 * c);
-            o[0] = make_float4(dg[i][0], dg[i][1], dg[i][2], dg[i][3]);
-            o[1] = make_float4(dg[i][4], dg[i][5], dg[i][6], dg[i][7]);
+            o[0] = make_float4(dg[i][0].x, dg[i][0].y, dg[i][1].x, dg[i][1].y);
+            o[1] = make_float4(dg[i][2].x, dg[i][2].y, dg[i][3].x, dg[i][3].y);
         }
     }
+    if (threadIdx.x == 0 && *wc.abort_flag)
+        drain(ring, pending, parity, p.wait_limit_ns);
 }
 
-// dgamma[c] = sum over the rows of part: 32 columns per CTA, 16 slices of the
-// rows summed side by side and then in slice order.
-constexpr int DG_SLICES = 16;
+// dgamma[c] = sum over the rows of part: 32 columns per CTA, 64 slices of the
+// rows side by side (slice s adds rows s, s + 64, ...), then the slices in
+// order, eight by eight.
+constexpr int DG_SLICES = 64;
+constexpr int DG_THREADS = 8 * DG_SLICES;
 
-__global__ void __launch_bounds__(32 * DG_SLICES) norm_dgamma_kernel(const float *__restrict__ part, int rows, int D,
-                                                                     float *__restrict__ dgamma)
+__global__ void __launch_bounds__(DG_THREADS) norm_dgamma_kernel(const float4 *__restrict__ part, int rows, int D,
+                                                                 float *__restrict__ dgamma)
 {
     griddep_launch_dependents();
     griddep_wait();
-    __shared__ float s[DG_SLICES][32];
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5;
-    float v = 0.0f;
-    for (int r = slice; r < rows; r += DG_SLICES)
-        v += part[(int64_t)r * D + c];
-    s[slice][threadIdx.x & 31] = v;
+    __shared__ float4 s[DG_SLICES][8];
+    __shared__ float s8[8][32];
+    const int c4 = threadIdx.x & 7, slice = threadIdx.x >> 3;
+    const float4 *col = part + blockIdx.x * 8 + c4;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+    for (int r = slice; r < rows; r += DG_SLICES) {
+        const float4 a = __ldg(col + (int64_t)r * (D / 4));
+        v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
+    }
+    s[slice][c4] = v;
     __syncthreads();
-    if (slice == 0) {
+    const float *f = reinterpret_cast<const float *>(&s[0][0]);
+    const int c = threadIdx.x & 31, oct = threadIdx.x >> 5;
+    if (oct < 8) {
+        float a = f[(8 * oct) * 32 + c];
 #pragma unroll
-        for (int i = 1; i < DG_SLICES; ++i)
-            v += s[i][threadIdx.x];
-        dgamma[c] = v;
+        for (int i = 1; i < 8; ++i)
+            a += f[(8 * oct + i) * 32 + c];
+        s8[oct][c] = a;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        float a = s8[0][c];
+#pragma unroll
+        for (int i = 1; i < 8; ++i)
+            a += s8[i][c];
+        dgamma[blockIdx.x * 32 + c] = a;
     }
 }
 
-// chunks per thread (the loads of a tensor that a thread has in flight) and
-// threads of a row of D columns
+// Width and threads of a row of D columns: up to four chunks per thread,
+// which share the row's reduction and the scales' division sequence.
 struct RowShape {
-    int cpt, threads;
+    int width, threads;
 };
 
 RowShape row_shape(int64_t D)
 {
     const int chunks = (int)(D / 8);
-    const int cpt = chunks <= 256 ? 1 : (chunks <= 1024 ? 2 : 3);
-    const int threads = ((chunks + cpt - 1) / cpt + 31) / 32 * 32;
-    return {cpt, threads};
+    const int width = chunks <= 32 ? ONE : (chunks <= 64 ? TWO : (chunks <= 4 * 256 ? FOUR : WIDE));
+    return {width, (chunks + 32 * cpt_of(width) - 1) / (32 * cpt_of(width)) * 32};
 }
 
-// CTAs of the forward kernel: what the device holds at once (48 registers a
-// thread), so that every CTA runs from the start and strides over the rows
-int fwd_grid(int64_t T, int threads)
+// CTAs per SM, slots of a CTA's ring and shared memory for rows of `tensors`
+// tensors.
+struct RingShape {
+    int per_sm, slots;
+    size_t smem;
+};
+
+// Forward: as many CTAs as the registers allow with two rows each in flight
+// (one row's reduction runs under another's loads and stores), or two CTAs with
+// three rows (8191 x 7168 with a residual: 64.6 us; three with two 67.8).
+// Backward: four rows each in flight rather than more CTAs, each of which adds
+// a row to dgamma's partial sums (16384 x 2048 with dres: 4 CTAs of 4 rows
+// 46 us, 8 of 2 60 us), down to two CTAs of two rows.
+RingShape ring_shape(int64_t D, int tensors, bool gamma_f32, bool bwd)
 {
-    const int per_sm = 1344 / threads < 1 ? 1 : (1344 / threads > 32 ? 32 : 1344 / threads);
-    const int64_t cap = (int64_t)sm_count() * per_sm;
+    const RowShape rs = row_shape(D);
+    const int64_t gamma_bytes = bwd && rs.width != WIDE ? (gamma_f32 ? 4 * D : 2 * D) : 0;
+    constexpr int64_t SM_BYTES = 226 * 1024;                      // of an SM
+    const int64_t beside = gamma_bytes + BAR_BYTES + 1024 + 512;  // of a CTA beside the ring, 1 KB of it the system's
+    const int64_t slot = 2 * D * tensors;
+    auto slots_of = [&](int per_sm) {
+        const int64_t n = (SM_BYTES / per_sm - beside) / slot;
+        return (int)(n > MAX_SLOTS ? MAX_SLOTS : n);
+    };
+    int per_sm = max_threads(rs.width) * min_ctas(rs.width, bwd) / rs.threads;
+    while (per_sm > 2 && slots_of(per_sm) < (bwd ? 4 : (per_sm == 3 ? 3 : 2)))
+        --per_sm;
+    if (slots_of(per_sm) < 2)
+        per_sm = 1;
+    const int slots = slots_of(per_sm);
+    return {per_sm, slots, (size_t)(slots * slot + BAR_BYTES + gamma_bytes)};
+}
+
+int ring_grid(int64_t T, const RingShape &r)
+{
+    const int64_t cap = (int64_t)sm_count() * r.per_sm;
     return (int)(T < cap ? T : (cap > 0 ? cap : 1));
 }
 
-// The backward kernel holds more per thread, and each CTA adds a row to the
-// partial sums of dgamma.
-int bwd_grid(int64_t T, int64_t D)
+template <typename K, typename P>
+int launch_ring(K k, const P &p, int grid, int threads, size_t smem, cudaStream_t s)
 {
-    const int threads = row_shape(D).threads;
-    const int per_sm = 896 / threads < 1 ? 1 : (896 / threads > 8 ? 8 : 896 / threads);
-    const int64_t cap = (int64_t)sm_count() * per_sm;
-    return (int)(T < cap ? T : (cap > 0 ? cap : 1));
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+        cudaGetLastError();
+        return FP8FG_ECUDA;
+    }
+    return launch_pss(k, dim3((unsigned)grid), threads, smem, s, p);
 }
 
-template <int CPT>
-int launch_fwd(const NormFwd &p, int grid, int threads, bool p2, cudaStream_t s)
+template <int W>
+int launch_fwd(const NormFwd &p, int grid, int threads, size_t smem, bool p2, cudaStream_t s)
 {
     if (p.r)
-        return p2 ? launch_pss(rmsnorm_fwd_kernel<CPT, true, true>, dim3(grid), threads, 0, s, p)
-                  : launch_pss(rmsnorm_fwd_kernel<CPT, true, false>, dim3(grid), threads, 0, s, p);
-    return p2 ? launch_pss(rmsnorm_fwd_kernel<CPT, false, true>, dim3(grid), threads, 0, s, p)
-              : launch_pss(rmsnorm_fwd_kernel<CPT, false, false>, dim3(grid), threads, 0, s, p);
+        return p2 ? launch_ring(rmsnorm_fwd_kernel<W, true, true>, p, grid, threads, smem, s)
+                  : launch_ring(rmsnorm_fwd_kernel<W, true, false>, p, grid, threads, smem, s);
+    return p2 ? launch_ring(rmsnorm_fwd_kernel<W, false, true>, p, grid, threads, smem, s)
+              : launch_ring(rmsnorm_fwd_kernel<W, false, false>, p, grid, threads, smem, s);
 }
 
-template <int CPT>
-int launch_bwd(const NormBwd &p, int grid, int threads, cudaStream_t s)
+template <int W>
+int launch_bwd(const NormBwd &p, int grid, int threads, size_t smem, cudaStream_t s)
 {
-    return p.dres ? launch_pss(rmsnorm_bwd_kernel<CPT, true>, dim3(grid), threads, 0, s, p)
-                  : launch_pss(rmsnorm_bwd_kernel<CPT, false>, dim3(grid), threads, 0, s, p);
+    return p.dres ? launch_ring(rmsnorm_bwd_kernel<W, true>, p, grid, threads, smem, s)
+                  : launch_ring(rmsnorm_bwd_kernel<W, false>, p, grid, threads, smem, s);
 }
 
 bool norm_width_ok(int64_t D) { return D >= 0 && D % GROUP == 0 && D <= NORM_MAX_D; }
@@ -445,12 +654,19 @@ extern "C" int fp8_rmsnorm(const void *x, int64_t ldx, const void *residual, int
     p.eps = eps;
     p.gamma_f32 = gamma_kind == FP8FG_OUT_F32;
     const RowShape rs = row_shape(D);
-    const int grid = fwd_grid(T, rs.threads);
+    const RingShape ring = ring_shape(D, residual ? 2 : 1, p.gamma_f32, false);
+    const int grid = ring_grid(T, ring);
+    p.slots = ring.slots;
+    p.status = status_word_ptr();
+    p.wait_limit_ns = wait_limit_ns();
+    if (!p.status)
+        return FP8FG_ECUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    switch (rs.cpt) {
-    case 1: return launch_fwd<1>(p, grid, rs.threads, pow2 != 0, s);
-    case 2: return launch_fwd<2>(p, grid, rs.threads, pow2 != 0, s);
-    default: return launch_fwd<3>(p, grid, rs.threads, pow2 != 0, s);
+    switch (rs.width) {
+    case ONE: return launch_fwd<ONE>(p, grid, rs.threads, ring.smem, pow2 != 0, s);
+    case TWO: return launch_fwd<TWO>(p, grid, rs.threads, ring.smem, pow2 != 0, s);
+    case FOUR: return launch_fwd<FOUR>(p, grid, rs.threads, ring.smem, pow2 != 0, s);
+    default: return launch_fwd<WIDE>(p, grid, rs.threads, ring.smem, pow2 != 0, s);
     }
 }
 
@@ -485,7 +701,8 @@ extern "C" int64_t fp8_rmsnorm_bwd_workspace(int64_t T, int64_t D)
 {
     if (T <= 0 || D <= 0 || !norm_width_ok(D))
         return 0;
-    return (int64_t)bwd_grid(T, D) * D * 4;
+    // the grid is largest without dres and with a bf16 gamma
+    return (int64_t)ring_grid(T, ring_shape(D, 2, false, true)) * D * 4;
 }
 
 extern "C" int fp8_rmsnorm_bwd(const void *dy, int64_t lddy, const void *h, int64_t ldh, const float *rstd,
@@ -522,7 +739,8 @@ extern "C" int fp8_rmsnorm_bwd(const void *dy, int64_t lddy, const void *h, int6
         return FP8FG_EALIGN;
     if (!device_supported())
         return FP8FG_EUNSUPPORTED;
-    const int grid = bwd_grid(T, D);
+    const RingShape ring = ring_shape(D, dres ? 3 : 2, gamma_kind == FP8FG_OUT_F32, true);
+    const int grid = ring_grid(T, ring);
     if (workspace_bytes < (int64_t)grid * D * 4)
         return FP8FG_EINVAL;
     NormBwd p{};
@@ -537,13 +755,20 @@ extern "C" int fp8_rmsnorm_bwd(const void *dy, int64_t lddy, const void *h, int6
     p.D = (int)D;
     p.gamma_f32 = gamma_kind == FP8FG_OUT_F32;
     const RowShape rs = row_shape(D);
+    p.slots = ring.slots;
+    p.status = status_word_ptr();
+    p.wait_limit_ns = wait_limit_ns();
+    if (!p.status)
+        return FP8FG_ECUDA;
     int rc;
-    switch (rs.cpt) {
-    case 1: rc = launch_bwd<1>(p, grid, rs.threads, s); break;
-    case 2: rc = launch_bwd<2>(p, grid, rs.threads, s); break;
-    default: rc = launch_bwd<3>(p, grid, rs.threads, s); break;
+    switch (rs.width) {
+    case ONE: rc = launch_bwd<ONE>(p, grid, rs.threads, ring.smem, s); break;
+    case TWO: rc = launch_bwd<TWO>(p, grid, rs.threads, ring.smem, s); break;
+    case FOUR: rc = launch_bwd<FOUR>(p, grid, rs.threads, ring.smem, s); break;
+    default: rc = launch_bwd<WIDE>(p, grid, rs.threads, ring.smem, s); break;
     }
     if (rc != FP8FG_OK)
         return rc;
-    return launch_pss(norm_dgamma_kernel, dim3((unsigned)(D / 32)), 32 * DG_SLICES, 0, s, p.part, grid, (int)D, dgamma);
+    return launch_pss(norm_dgamma_kernel, dim3((unsigned)(D / 32)), DG_THREADS, 0, s,
+                      reinterpret_cast<const float4 *>(p.part), grid, (int)D, dgamma);
 }

@@ -7,8 +7,8 @@ of squares, 17 u after the root, plus 4 u for the division, the addition and
 rsqrtf: at most 24 u. y = h * rstd * gamma adds two products: 26 u |y|.
 dx: the row's dot product carries 36 u of its absolute terms, the remaining
 steps 8 u: 50 u of the bound tx, then half a bf16 ulp. dgamma: a CTA adds
-ceil(T / 152) rows, at most 8 * 152 partial rows are added 16 apart and the 16
-sums last: (T / 152 + 1 + 76 + 16 + 4) u of the absolute terms."""
+ceil(T / grid) rows, the CTAs' sums are added at most 97 deep (T / 152 + 97) u
+of the absolute terms."""
 import numpy as np
 import pytest
 import torch
