@@ -13,9 +13,13 @@
 // is still in L2.
 //
 // The tensors' pointers and sizes travel in the kernels' parameters (no device
-// table to copy). A tensor is cut into chunks of CHUNK elements whose vector
-// loads start on a 16-byte boundary of its own; the elements before the first
-// boundary belong to chunk 0. Chunks are dealt round-robin to the CTAs.
+// table to copy). A tensor is cut into chunks of bytes whose vector loads start
+// on a 16-byte boundary of its own; the elements before the first boundary
+// belong to chunk 0. Chunks are dealt round-robin to the CTAs. Both kernels run
+// best with few CTAs that each keep a whole chunk in flight (UNROLL 16-byte
+// loads per thread): for 400 M FP32 elements, sums with 2 CTAs per SM of 64 KB
+// chunks 256 us, 4 of 32 KB 280; scaling with 2 of 32 KB 428 us, 2 of 64 KB
+// 496, 4 of 32 KB 530.
 #include <cuda_bf16.h>
 
 #include "host_common.h"
@@ -24,9 +28,10 @@
 namespace fp8fg {
 namespace {
 
-constexpr int CHUNK = 8192;
 constexpr int THREADS = 256;
-constexpr int CTAS_PER_SM = 4;
+constexpr int CTAS_PER_SM = 2;
+constexpr int SUM_UNROLL = 16, SCALE_UNROLL = 8;
+constexpr int chunk_bytes(int unroll) { return unroll * THREADS * 16; }
 constexpr int MAX_TENSORS = 1024;  // per launch: 24 bytes + 4 each in the 32 KB of kernel parameters
 
 template <int N>
@@ -51,28 +56,33 @@ __host__ __device__ __forceinline__ int head_elements(const void *p, int esz)
     return (int)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / esz;
 }
 
-template <int N>
-__device__ __forceinline__ Piece piece_of(const Table<N> &tab, uint32_t chunk)
+// Piece of a chunk. `cur` is the tensor of the CTA's previous chunk, mostly
+// this one's too; else the last tensor with first <= chunk is searched for.
+template <int N, int UNROLL>
+__device__ __forceinline__ Piece piece_of(const Table<N> &tab, uint32_t chunk, int &cur)
 {
-    int lo = 0, hi = tab.count;  // last tensor with first <= chunk
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (tab.first[mid] <= chunk)
-            lo = mid;
-        else
-            hi = mid;
+    if (chunk < tab.first[cur] || chunk >= tab.first[cur + 1]) {
+        int lo = 0, hi = tab.count;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (tab.first[mid] <= chunk)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        cur = lo;
     }
     Piece q;
-    q.bf16 = tab.n[lo] < 0;
-    const int64_t n = q.bf16 ? -tab.n[lo] : tab.n[lo];
-    q.g = static_cast<const uint8_t *>(tab.g[lo]);
-    q.out = static_cast<uint8_t *>(tab.out[lo]);
+    q.bf16 = tab.n[cur] < 0;
+    const int64_t n = q.bf16 ? -tab.n[cur] : tab.n[cur];
+    q.g = static_cast<const uint8_t *>(tab.g[cur]);
+    q.out = static_cast<uint8_t *>(tab.out[cur]);
     int64_t head = head_elements(q.g, q.bf16 ? 2 : 4);
     head = head < n ? head : n;
-    const int64_t at = (int64_t)(chunk - tab.first[lo]) * CHUNK;
+    const int64_t per = chunk_bytes(UNROLL) / (q.bf16 ? 2 : 4), at = (int64_t)(chunk - tab.first[cur]) * per;
     q.head = at == 0 ? (int)head : 0;
     q.begin = head + at;
-    q.end = q.begin + CHUNK < n ? q.begin + CHUNK : n;
+    q.end = q.begin + per < n ? q.begin + per : n;
     return q;
 }
 
@@ -99,16 +109,22 @@ __device__ __forceinline__ uint4 ld16(const void *p)
     return v;
 }
 
-__device__ __forceinline__ float sq16(const uint4 &v, bool bf16)
+// s += the squares of 16 bytes
+__device__ __forceinline__ float2 sq16(const uint4 &v, bool bf16, float2 s)
 {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    float s = 0.0f;
+    if (bf16) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (bf16)
-            s = fmaf(bf16_lo(w[i]), bf16_lo(w[i]), fmaf(bf16_hi(w[i]), bf16_hi(w[i]), s));
-        else
-            s = fmaf(__uint_as_float(w[i]), __uint_as_float(w[i]), s);
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = make_float2(bf16_lo(w[i]), bf16_hi(w[i]));
+            s = __ffma2_rn(f, f, s);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            const float2 f = make_float2(__uint_as_float(w[i]), __uint_as_float(w[i + 1]));
+            s = __ffma2_rn(f, f, s);
+        }
     }
     return s;
 }
@@ -144,10 +160,8 @@ __device__ __forceinline__ double block_sum(double v, double *part)
     return v;
 }
 
-constexpr int UNROLL = 8;  // 16-byte loads of a thread in flight
-
-// Squares are FP32, summed in FP32 inside a chunk (32 terms or fewer per
-// thread) and in FP64 beyond it.
+// Squares are FP32, summed in FP32 inside a chunk (eight sums of at most 16
+// terms per thread, then those) and in FP64 beyond it.
 template <int N>
 __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     sumsq_kernel(const __grid_constant__ Table<N> tab, double *partial)
@@ -156,25 +170,29 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     griddep_wait();
     __shared__ double part[THREADS / 32];
     const uint32_t chunks = tab.first[tab.count];
+    constexpr int UNROLL = SUM_UNROLL;
     double total = 0.0;
+    int cur = 0;
     for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-        const Piece q = piece_of(tab, c);
+        const Piece q = piece_of<N, UNROLL>(tab, c, cur);
         const int esz = q.bf16 ? 2 : 4, per = 16 / esz;
         const int64_t len = q.end - q.begin;
         const int vecs = len > 0 ? (int)(len / per) : 0;
         const uint8_t *src = q.g + q.begin * esz;
-        float s = 0.0f;
-        for (int i0 = 0; i0 < vecs; i0 += UNROLL * THREADS) {
-            uint4 v[UNROLL];
+        uint4 v[UNROLL];
 #pragma unroll
-            for (int j = 0; j < UNROLL; ++j) {
-                const int i = i0 + j * THREADS + threadIdx.x;
-                v[j] = i < vecs ? ld16(src + (int64_t)i * 16) : make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int j = 0; j < UNROLL; ++j)
-                s += sq16(v[j], q.bf16);
+        for (int j = 0; j < UNROLL; ++j) {
+            const int i = j * THREADS + threadIdx.x;
+            v[j] = i < vecs ? ld16(src + i * 16) : make_uint4(0, 0, 0, 0);
         }
+        float2 s2[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            s2[j] = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int j = 0; j < UNROLL; ++j)
+            s2[j & 3] = sq16(v[j], q.bf16, s2[j & 3]);
+        float s = ((s2[0].x + s2[0].y) + (s2[1].x + s2[1].y)) + ((s2[2].x + s2[2].y) + (s2[3].x + s2[3].y));
         const int tail = len > 0 ? (int)(len - (int64_t)vecs * per) : 0;
         if ((int)threadIdx.x < tail) {
             const float v = load_one(q.g, q.begin + (int64_t)vecs * per + threadIdx.x, q.bf16);
@@ -203,16 +221,19 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     for (int i = threadIdx.x; i < n_partial; i += THREADS)
         total += partial[i];
     total = block_sum(total, part);
-    const float norm = (float)sqrt(total);
+    // root in FP32, of the sum brought into its range
+    const float norm = total > 1e30 ? sqrtf((float)(total * 0x1p-200)) * 0x1p100f : sqrtf((float)total);
     const float ratio = max_norm / (norm + eps);
     const float coef = ratio > 1.0f ? 1.0f : ratio;  // a NaN norm gives NaN
     if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) {
         norm_out[0] = norm;
         norm_out[1] = coef;
     }
+    constexpr int UNROLL = SCALE_UNROLL;
     const uint32_t chunks = tab.first[tab.count];
+    int cur = 0;
     for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-        const Piece q = piece_of(tab, chunks - 1 - c);
+        const Piece q = piece_of<N, UNROLL>(tab, chunks - 1 - c, cur);
         if (coef == 1.0f && q.out == q.g)
             continue;
         const int esz = q.bf16 ? 2 : 4, per = 16 / esz;
@@ -222,20 +243,18 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
         const int vecs = len > 0 && same ? (int)(len / per) : 0;
         const uint8_t *src = q.g + q.begin * esz;
         uint8_t *dst = q.out + q.begin * esz;
-        for (int i0 = 0; i0 < vecs; i0 += UNROLL * THREADS) {
-            uint4 v[UNROLL];
+        uint4 v[UNROLL];
 #pragma unroll
-            for (int j = 0; j < UNROLL; ++j) {
-                const int i = i0 + j * THREADS + threadIdx.x;
-                if (i < vecs)
-                    v[j] = ld16(src + (int64_t)i * 16);
-            }
+        for (int j = 0; j < UNROLL; ++j) {
+            const int i = j * THREADS + threadIdx.x;
+            if (i < vecs)
+                v[j] = ld16(src + i * 16);
+        }
 #pragma unroll
-            for (int j = 0; j < UNROLL; ++j) {
-                const int i = i0 + j * THREADS + threadIdx.x;
-                if (i < vecs)
-                    *reinterpret_cast<uint4 *>(dst + (int64_t)i * 16) = mul16(v[j], q.bf16, coef);
-            }
+        for (int j = 0; j < UNROLL; ++j) {
+            const int i = j * THREADS + threadIdx.x;
+            if (i < vecs)
+                __stcs(reinterpret_cast<uint4 *>(dst + i * 16), mul16(v[j], q.bf16, coef));
         }
         for (int64_t i = q.begin + (int64_t)vecs * per + threadIdx.x; i < q.end; i += THREADS)
             store_one(q.out, i, q.bf16, load_one(q.g, i, q.bf16) * coef);
@@ -244,21 +263,29 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     }
 }
 
+// CTAs of a launch: all resident at once.
 int64_t grid_cap()
 {
     const int sms = sm_count();
     return (int64_t)(sms > 0 ? sms : 1) * CTAS_PER_SM;
 }
 
-int64_t chunks_of(const fp8fg_grad &t)
+unsigned grid_of(int64_t chunks)
 {
-    const int64_t body = t.n - head_elements(t.g, t.kind == FP8FG_OUT_BF16 ? 2 : 4);
-    return body > CHUNK ? (body + CHUNK - 1) / CHUNK : 1;
+    const int64_t cap = grid_cap();
+    return (unsigned)(chunks < cap ? (chunks > 0 ? chunks : 1) : cap);
 }
 
-// Tensors [at, at + take) of one launch; their chunks fit in 31 bits
+int64_t chunks_of(const fp8fg_grad &t, int unroll)
+{
+    const int esz = t.kind == FP8FG_OUT_BF16 ? 2 : 4;
+    const int64_t body = (t.n - head_elements(t.g, esz)) * esz, per = chunk_bytes(unroll);
+    return t.n == 0 ? 0 : (body > per ? (body + per - 1) / per : 1);
+}
+
+// Tensors [0, take) of one launch; their chunks fit in 31 bits
 template <int N>
-void fill(Table<N> &tab, const fp8fg_grad *t, int take)
+void fill(Table<N> &tab, const fp8fg_grad *t, int take, int unroll)
 {
     uint32_t first = 0;
     for (int i = 0; i < take; ++i) {
@@ -266,8 +293,7 @@ void fill(Table<N> &tab, const fp8fg_grad *t, int take)
         tab.out[i] = t[i].out;
         tab.n[i] = t[i].kind == FP8FG_OUT_BF16 ? -t[i].n : t[i].n;
         tab.first[i] = first;
-        if (t[i].n > 0)
-            first += (uint32_t)chunks_of(t[i]);
+        first += (uint32_t)chunks_of(t[i], unroll);
     }
     tab.first[take] = first;
     tab.count = take;
@@ -278,10 +304,10 @@ template <int N>
 int launch_sumsq(const fp8fg_grad *t, int take, double *partial, int *used, cudaStream_t s)
 {
     Table<N> tab;
-    fill(tab, t, take);
-    const int64_t chunks = tab.first[take];
-    *used = (int)(chunks < grid_cap() ? (chunks > 0 ? chunks : 1) : grid_cap());
-    return launch_pss(sumsq_kernel<N>, dim3((unsigned)*used), THREADS, 0, s, tab, partial);
+    fill(tab, t, take, SUM_UNROLL);
+    const unsigned grid = grid_of(tab.first[take]);
+    *used = (int)grid;
+    return launch_pss(sumsq_kernel<N>, dim3(grid), THREADS, 0, s, tab, partial);
 }
 
 template <int N>
@@ -289,10 +315,8 @@ int launch_scale(const fp8fg_grad *t, int take, const double *partial, int n_par
                  float *norm, cudaStream_t s)
 {
     Table<N> tab;
-    fill(tab, t, take);
-    const int64_t chunks = tab.first[take];
-    const int64_t grid = chunks < grid_cap() ? (chunks > 0 ? chunks : 1) : grid_cap();
-    return launch_pss(scale_kernel<N>, dim3((unsigned)grid), THREADS, 0, s, tab, partial, n_partial, max_norm, eps, norm);
+    fill(tab, t, take, SCALE_UNROLL);
+    return launch_pss(scale_kernel<N>, dim3(grid_of(tab.first[take])), THREADS, 0, s, tab, partial, n_partial, max_norm, eps, norm);
 }
 
 }  // namespace
@@ -339,7 +363,7 @@ extern "C" int fp8fg_grad_clip(const fp8fg_grad *grads, int64_t count, float max
             const int take = (int)(count - at < MAX_TENSORS ? count - at : MAX_TENSORS);
             int64_t chunks = 0;
             for (int i = 0; i < take; ++i)
-                chunks += chunks_of(grads[at + i]);
+                chunks += chunks_of(grads[at + i], SCALE_UNROLL);
             if (chunks >= (1ll << 31))
                 return FP8FG_EINVAL;
             int rc;

@@ -47,6 +47,15 @@ struct Smem {
     int abort;
 };
 
+// (volatile: the inputs are in registers before the barrier that lets the next
+// tile overwrite them)
+__device__ __forceinline__ uint2 lds8(const uint16_t *p)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(smem_u32(p)));
+    return v;
+}
+
 struct Params {
     int64_t tiles_c, n_tiles, I;
     uint8_t *q;
@@ -109,25 +118,35 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             return;
         }
-        // v[0] = dG, v[1] = dU, v[2] = h
-        float v[3][ROWS][4];
+        uint2 gw[ROWS], uw[ROWS], dw[ROWS];
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
             const int row = warp * ROWS + i;
-            const uint2 gw = *reinterpret_cast<const uint2 *>(&S.in[0][row][4 * lane]);
-            const uint2 uw = *reinterpret_cast<const uint2 *>(&S.in[1][row][4 * lane]);
-            const uint2 dw = *reinterpret_cast<const uint2 *>(&S.in[2][row][4 * lane]);
-            const float g[4] = {bf16_lo(gw.x), bf16_hi(gw.x), bf16_lo(gw.y), bf16_hi(gw.y)};
-            const float u[4] = {bf16_lo(uw.x), bf16_hi(uw.x), bf16_lo(uw.y), bf16_hi(uw.y)};
-            const float d[4] = {bf16_lo(dw.x), bf16_hi(dw.x), bf16_lo(dw.y), bf16_hi(dw.y)};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float sg = sigmoid(g[j]), a = g[j] * sg;
-                v[0][i][j] = d[j] * u[j] * fmaf(a, 1.0f - sg, sg);
-                v[1][i][j] = d[j] * a;
-                v[2][i][j] = a * u[j];
-            }
+            gw[i] = lds8(&S.in[0][row][4 * lane]);
+            uw[i] = lds8(&S.in[1][row][4 * lane]);
+            dw[i] = lds8(&S.in[2][row][4 * lane]);
         }
+        __syncthreads();
+        // every thread holds its inputs: the next tile may land
+        if (tid == 0 && t + gridDim.x < p.n_tiles)
+            fetch(t + gridDim.x);
+        // v[0] = dG, v[1] = dU, v[2] = h, in pairs of columns
+        float2 v[3][ROWS][2];
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t gb = j ? gw[i].y : gw[i].x, ub = j ? uw[i].y : uw[i].x, db = j ? dw[i].y : dw[i].x;
+                const float2 g = make_float2(bf16_lo(gb), bf16_hi(gb));
+                const float2 u = make_float2(bf16_lo(ub), bf16_hi(ub));
+                const float2 d = make_float2(bf16_lo(db), bf16_hi(db));
+                const float2 sg = make_float2(sigmoid(g.x), sigmoid(g.y));
+                const float2 a = __fmul2_rn(g, sg);
+                const float2 rest = __ffma2_rn(sg, make_float2(-1.0f, -1.0f), make_float2(1.0f, 1.0f));
+                v[0][i][j] = __fmul2_rn(__fmul2_rn(d, u), __ffma2_rn(a, rest, sg));
+                v[1][i][j] = __fmul2_rn(d, a);
+                v[2][i][j] = __fmul2_rn(a, u);
+            }
         // column maxima of this warp's rows
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
@@ -135,14 +154,13 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int i = 0; i < ROWS; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    m[j] = fmaxf(m[j], fabsf(v[k][i][j]));
+                for (int j = 0; j < 2; ++j) {
+                    m[2 * j] = fmaxf(m[2 * j], fabsf(v[k][i][j].x));
+                    m[2 * j + 1] = fmaxf(m[2 * j + 1], fabsf(v[k][i][j].y));
+                }
             *reinterpret_cast<float4 *>(&S.cmax[k][warp][4 * lane]) = make_float4(m[0], m[1], m[2], m[3]);
         }
         __syncthreads();
-        // every thread has read its inputs: the next tile may land
-        if (tid == 0 && t + gridDim.x < p.n_tiles)
-            fetch(t + gridDim.x);
         // column groups: one thread each
         if (tid < 3 * GROUP) {
             const int k = tid / GROUP, c = tid % GROUP;
@@ -165,8 +183,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int i = 0; i < ROWS; ++i) {
-                const float m = fmaxf(fmaxf(fabsf(v[k][i][0]), fabsf(v[k][i][1])),
-                                      fmaxf(fabsf(v[k][i][2]), fabsf(v[k][i][3])));
+                const float m = fmaxf(fmaxf(fabsf(v[k][i][0].x), fabsf(v[k][i][0].y)),
+                                      fmaxf(fabsf(v[k][i][1].x), fabsf(v[k][i][1].y)));
                 const uint32_t r = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
                 mine = (lane & 15) == ROWS * k + i ? __uint_as_float(r) : mine;
             }
@@ -180,8 +198,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int i = 0; i < ROWS; ++i) {
                 const float inv = __shfl_sync(0xffffffffu, rp.inv, ROWS * k + i);
-                const uint32_t w = cvt_e4m3x2(v[k][i][0] * inv, v[k][i][1] * inv) |
-                                   (cvt_e4m3x2(v[k][i][2] * inv, v[k][i][3] * inv) << 16);
+                const float2 lo = __fmul2_rn(v[k][i][0], make_float2(inv, inv));
+                const float2 hi = __fmul2_rn(v[k][i][1], make_float2(inv, inv));
+                const uint32_t w = cvt_e4m3x2(lo.x, lo.y) | (cvt_e4m3x2(hi.x, hi.y) << 16);
                 *reinterpret_cast<uint32_t *>(p.q + (r0 + warp * ROWS + i) * p.ldq + k * p.I + c0 + 4 * lane) = w;
             }
         __syncthreads();
@@ -191,15 +210,22 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
             const float4 iv = *reinterpret_cast<const float4 *>(&S.cinv[k][4 * lane]);
-            const float inv[4] = {iv.x, iv.y, iv.z, iv.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t w[2];
+            for (int j = 0; j < 2; ++j) {
+                const float2 inv = j ? make_float2(iv.z, iv.w) : make_float2(iv.x, iv.y);
+                uint32_t w0[2], w1[2];  // columns 2j and 2j + 1
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    w[h] = cvt_e4m3x2(v[k][4 * h][j] * inv[j], v[k][4 * h + 1][j] * inv[j]) |
-                           (cvt_e4m3x2(v[k][4 * h + 2][j] * inv[j], v[k][4 * h + 3][j] * inv[j]) << 16);
-                *reinterpret_cast<uint2 *>(&S.codes[k][4 * lane + j][8 * (warp ^ (lane & 15))]) = make_uint2(w[0], w[1]);
+                for (int h = 0; h < 2; ++h) {
+                    float2 s2[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        s2[i] = __fmul2_rn(v[k][4 * h + i][j], inv);
+                    w0[h] = cvt_e4m3x2(s2[0].x, s2[1].x) | (cvt_e4m3x2(s2[2].x, s2[3].x) << 16);
+                    w1[h] = cvt_e4m3x2(s2[0].y, s2[1].y) | (cvt_e4m3x2(s2[2].y, s2[3].y) << 16);
+                }
+                const int piece = 8 * (warp ^ (lane & 15));
+                *reinterpret_cast<uint2 *>(&S.codes[k][4 * lane + 2 * j][piece]) = make_uint2(w0[0], w0[1]);
+                *reinterpret_cast<uint2 *>(&S.codes[k][4 * lane + 2 * j + 1][piece]) = make_uint2(w1[0], w1[1]);
             }
         }
         __syncthreads();

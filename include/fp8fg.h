@@ -562,8 +562,9 @@ FP8FG_API int fp8_gated_bwd(const void *gu, int64_t ldgu, const void *dh, int64_
  *   norm    FP32 [2], device: the norm and coef.
  *   workspace  8-byte aligned, at least fp8fg_grad_clip_workspace(count)
  *           bytes on the current device.
- *   Squares are FP32 and are added up in FP32 over at most 32 elements of a
- *   thread, in FP64 beyond; the order is fixed, so the result does not vary
+ *   Squares are FP32 and are added up in FP32 inside a thread's part of 64 KB
+ *   (sums 16 terms deep), in FP64 beyond; the order is fixed, so the result
+ *   does not vary
  *   between calls. Elements beyond 1.8e19 in magnitude give an infinite norm
  *   (coef 0), a NaN gives NaN everywhere; elements below 1e-23 count as zero
  *   in the norm.

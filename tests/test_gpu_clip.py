@@ -1,8 +1,8 @@
 """GPU parity of grad_clip against 64-bit forms.
 
-Error bounds (u = 2^-24): a thread adds at most 8 vectors of 8 squares in
-FP32, 8 terms inside a vector and 8 sums, plus two single elements: 20 u on
-the sum of squares, 10 u on the norm after the root, 2 u for its rounding; the
+Error bounds (u = 2^-24): a thread adds 16 squares in sequence and three
+levels of such sums in FP32, plus two single elements: at most 21 u on the sum
+of squares, 10.5 u on the norm after the root, 1.5 u for the root; the
 factor adds an addition and a quotient: 14 u; the product one more: 15 u, and
 half a bf16 ulp for bf16 tensors."""
 import math
