@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const float2 g = make_float2(bf16_lo(gb), bf16_hi(gb));
                 const float2 u = make_float2(bf16_lo(ub), bf16_hi(ub));
                 const float2 d = make_float2(bf16_lo(db), bf16_hi(db));
-                const float2 sg = make_float2(sigmoid(g.x), sigmoid(g.y));
+                const float2 sg = sigmoid2(g);
                 const float2 a = __fmul2_rn(g, sg);
                 const float2 rest = __ffma2_rn(sg, make_float2(-1.0f, -1.0f), make_float2(1.0f, 1.0f));
                 v[0][i][j] = __fmul2_rn(__fmul2_rn(d, u), __ffma2_rn(a, rest, sg));
@@ -246,10 +246,9 @@ template <bool P2>
 int launch(const CUtensorMap &gu, const CUtensorMap &dh, const Params &p, cudaStream_t s)
 {
     auto k = gated_bwd_kernel<P2>;
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem)) != cudaSuccess) {
-        cudaGetLastError();
+    static std::atomic<uint64_t> done{0};
+    if (!allow_smem(k, sizeof(Smem), done))
         return FP8FG_ECUDA;
-    }
     const int64_t sms = sm_count();
     const unsigned grid = (unsigned)(p.n_tiles < sms ? p.n_tiles : (sms > 0 ? sms : 1));
     return launch_pss(k, dim3(grid), THREADS, sizeof(Smem), s, gu, dh, p);

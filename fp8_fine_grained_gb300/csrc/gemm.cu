@@ -565,57 +565,56 @@ __device__ __forceinline__ void skinny_roles(const CUtensorMap *tmX, const CUten
 // Epilogue of a GATED tile for one promotion warp: acc[0..31] are the gate
 // sums and acc[32..63] the up sums of the thread's row at columns col0 ..
 // col0+63 of h. Stores the two projections in bf16 when asked for, then
-//   h = gate * sigmoid(gate) * up        (silu_mul)
+//   h = gate * sigmoid(gate) * up
 // in FP32 and its E4M3 codes. The 128 columns of a scale group lie in the two
 // warps of the row's lane quarter: they exchange their row maxima through
 // shared memory, ordered by a barrier of the pair. A warp can be one exchange
 // ahead of its partner at most, so two sets of maxima suffice. All stores pass
-// through the warp's staging block as in the other epilogues. Returns false
-// when the (bounded) wait for the partner ran out.
+// through the warp's staging block as in the other epilogues (whole 32-byte
+// sectors straight from the registers were within 1 %). Returns false when the
+// (bounded) wait for the partner ran out. The gate and the exchange cost
+// nothing measurable: 4096 x 7168 x 18432 takes 839 us, 867 with gu, and the
+// plain product of the same size 870 (2.16 TFLOP, 2.5 PFLOP/s).
 template <class L>
 __device__ __forceinline__ bool gated_epilogue(const Params &p, uint8_t *smem, float2 (&acc)[64], int64_t row,
                                                bool row_ok, const Tile &tl, int64_t col0, int ew, int lane,
                                                uint32_t xphase, const WaitCtl &wc)
 {
     uint8_t *const stg = smem + L::stage_c_off + ew * STAGE_C_BYTES;
-    uint8_t *const w_row = stg + lane * 64;
-    const int w_sw = (lane >> 1) & 3;
-    const int cc = lane & 3;
-    const uint8_t *const r_ptr = stg + (lane >> 2) * 64 + ((cc ^ ((lane >> 3) & 3)) << 4);
-    const int64_t rrow0 = row - lane + (lane >> 2);
-    // 64 bytes of each of the warp's rows, from `o` to `base` (of row rrow0)
-    auto store_piece = [&](const uint4 (&o)[4], uint8_t *base, int64_t pitch) {
+    // 64 bytes of each of the warp's rows to column byte `at` of a matrix
+    auto store_piece = [&](const uint32_t(&w)[16], uint8_t *base, int64_t pitch, int64_t at) {
+        const int cc = lane & 3;
+        const int64_t rrow0 = row - lane + (lane >> 2);
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-            *reinterpret_cast<uint4 *>(w_row + ((c ^ w_sw) << 4)) = o[c];
+            *reinterpret_cast<uint4 *>(stg + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
+                make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(r_ptr + i * 512);
+            const uint4 v = *reinterpret_cast<const uint4 *>(stg + i * 512 + (lane >> 2) * 64 +
+                                                             ((cc ^ ((lane >> 3) & 3)) << 4));
             if (rrow0 + 8 * i < tl.row_end)
-                *reinterpret_cast<uint4 *>(base + 8 * i * pitch + cc * 16) = v;
+                *reinterpret_cast<uint4 *>(base + (rrow0 + 8 * i) * pitch + at + cc * 16) = v;
         }
         __syncwarp();
     };
     if (p.gu) {
-        uint8_t *const out = reinterpret_cast<uint8_t *>(p.gu + rrow0 * p.ld_gu + col0);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            uint4 o[4];
-            uint32_t *w = reinterpret_cast<uint32_t *>(o);
+            uint32_t w[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
                 const __nv_bfloat162 b = __float22bfloat162_rn(acc[16 * q + k]);
                 w[k] = *reinterpret_cast<const uint32_t *>(&b);
             }
-            store_piece(o, out + (q >> 1) * p.N * 2 + (q & 1) * 64, p.ld_gu * 2);
+            store_piece(w, reinterpret_cast<uint8_t *>(p.gu), p.ld_gu * 2, 2 * (col0 + (q >> 1) * p.N) + (q & 1) * 64);
         }
     }
     float amax = 0.0f;
 #pragma unroll
     for (int a = 0; a < 32; ++a) {
-        acc[a].x = silu_mul(acc[a].x, acc[32 + a].x);
-        acc[a].y = silu_mul(acc[a].y, acc[32 + a].y);
+        acc[a] = silu_mul2(acc[a], acc[32 + a]);
         amax = fmaxf(amax, fmaxf(fabsf(acc[a].x), fabsf(acc[a].y)));
     }
     const int quarter = ew & 3, half = ew >> 2;
@@ -631,13 +630,14 @@ __device__ __forceinline__ bool gated_epilogue(const Params &p, uint8_t *smem, f
     const ScalePair sp = p.out_pow2 ? group_scale_pow2(amax) : group_scale(amax);
     if (half == 0 && row_ok)
         p.sC[(tl.n0 / 128) * p.ld_sC + row] = sp.s;
-    uint4 o[4];
-    uint32_t *w = reinterpret_cast<uint32_t *>(o);
+    const float2 inv = make_float2(sp.inv, sp.inv);
+    uint32_t w[16];
 #pragma unroll
-    for (int k = 0; k < 16; ++k)
-        w[k] = cvt_e4m3x2(__fmul_rn(acc[2 * k].x, sp.inv), __fmul_rn(acc[2 * k].y, sp.inv)) |
-               (cvt_e4m3x2(__fmul_rn(acc[2 * k + 1].x, sp.inv), __fmul_rn(acc[2 * k + 1].y, sp.inv)) << 16);
-    store_piece(o, static_cast<uint8_t *>(p.C) + rrow0 * p.ldc + col0, p.ldc);
+    for (int k = 0; k < 16; ++k) {
+        const float2 a = __fmul2_rn(acc[2 * k], inv), b = __fmul2_rn(acc[2 * k + 1], inv);
+        w[k] = cvt_e4m3x2(a.x, a.y) | (cvt_e4m3x2(b.x, b.y) << 16);
+    }
+    store_piece(w, static_cast<uint8_t *>(p.C), p.ldc, col0);
     return true;
 }
 
@@ -834,10 +834,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                             if (second_half)
                                 tma_load_2d(b_dst + B_STAGE_BYTES / 2, &tmB, (int32_t)tl.n0 + 128, kb * BK, fb);
                         } else if constexpr (MODE == GATED) {
-#pragma unroll
-                            for (int r = 0; r < BN / GATED_RUN; ++r)
-                                tma_load_2d(b_dst + r * GATED_RUN * BK, &tmB, kb * BK,
-                                            (int32_t)(tl.n0 + (r & 1) * p.N + (r >> 1) * GATED_RUN), fb);
+                            // 64 rows x {gate, up} x 2 runs in one copy (four
+                            // boxes of 64 rows: 898 us instead of 839 for 4096
+                            // x 7168 x 18432 without gu)
+                            tma_load_4d(b_dst, &tmB, kb * BK, 0, 0, (int32_t)(tl.n0 / GATED_RUN), fb);
                         } else {
                             tma_load_2d(b_dst, &tmB, kb * BK, (int32_t)tl.n0, fb);
                         }
@@ -1460,8 +1460,11 @@ int gated_gemm_tiles(const GatedArgs &g, cudaStream_t s)
     if (!fill_runtime(p))
         return FP8FG_ECUDA;
     Maps m;
+    const uint64_t dims[3] = {GATED_RUN, 2, (uint64_t)g.I / GATED_RUN};
+    const uint64_t strides[3] = {1, (uint64_t)g.I, GATED_RUN};
+    const uint32_t box[3] = {GATED_RUN, 2, 2};
     if (!make_map(&m.a, g.xq, (uint64_t)g.K, (uint64_t)g.M, (uint64_t)g.ldx, BK, BM) ||
-        !make_map(&m.b, g.wq, (uint64_t)g.K, (uint64_t)(2 * g.I), (uint64_t)g.ldw, BK, GATED_RUN) ||
+        !make_map_rows(&m.b, g.wq, (uint64_t)g.K, (uint64_t)g.ldw, 3, dims, strides, BK, box) ||
         !make_map_f32_row(&m.sa, g.sx, (uint64_t)g.M, (uint64_t)(g.K / BK), (uint64_t)g.ld_sx, SA_BOX))
         return FP8FG_ECUDA;
     m.sb = m.sa;  // unused

@@ -89,9 +89,9 @@ template <int TILING> struct Shape {
     // setmaxnreg moves them from warps 0..3 to the promotion warps (the
     // launch's total bounds it)
     static constexpr bool REBALANCE = TILING == ROWS;
-    static constexpr int LOW = 56, HIGH = 224;
-    static constexpr int LAUNCH_MIN = (128 * LOW + PROMO_WARPS * 32 * HIGH + THREADS - 1) / THREADS;
 };
+constexpr int LOW = 56, HIGH = 224;  // registers per thread after the move
+constexpr int LAUNCH_MIN = (128 * LOW + PROMO_WARPS * 32 * HIGH + THREADS - 1) / THREADS;
 
 struct ClusterParams {
     int64_t M, I, K;
@@ -131,7 +131,7 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank)
 // the gate and the codes. NT tokens of a warp share one division sequence for
 // their scales (lane n on token n); with one per token the divisions are a
 // third of this part's instructions. ROWS, 333 tokens through 7168 x 2048: NT
-// = 8 19.2 us, NT = 1 19.8; FEW has a token or two per warp and takes NT = 1.
+// = 8 18.7 us, NT = 1 19.3; FEW has a token or two per warp and takes NT = 1.
 template <uint32_t PITCH, int NT>
 __device__ __forceinline__ void finish_tokens(const ClusterParams &p, uint32_t sbase, int rank, int warp, int lane,
                                               int nrows, int64_t m0, int64_t i0)
@@ -161,10 +161,9 @@ __device__ __forceinline__ void finish_tokens(const ClusterParams &p, uint32_t s
                 *reinterpret_cast<uint2 *>(p.gu + (m0 + j) * p.ld_gu + col) = o;
                 *reinterpret_cast<uint2 *>(p.gu + (m0 + j) * p.ld_gu + p.I + col) = q;
             }
-            v[n][0] = silu_mul(g.x, u.x);
-            v[n][1] = silu_mul(g.y, u.y);
-            v[n][2] = silu_mul(g.z, u.z);
-            v[n][3] = silu_mul(g.w, u.w);
+            const float2 lo = silu_mul2(make_float2(g.x, g.y), make_float2(u.x, u.y));
+            const float2 hi = silu_mul2(make_float2(g.z, g.w), make_float2(u.z, u.w));
+            v[n][0] = lo.x, v[n][1] = lo.y, v[n][2] = hi.x, v[n][3] = hi.y;
             const float m = fmaxf(fmaxf(fabsf(v[n][0]), fabsf(v[n][1])), fmaxf(fabsf(v[n][2]), fabsf(v[n][3])));
             const uint32_t amax = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
             mine = lane == n ? __uint_as_float(amax) : mine;
@@ -233,7 +232,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == 0) {
         // ------------------------------------------------------ producer ----
         if constexpr (SH::REBALANCE)
-            setmaxnreg_dec<SH::LOW>();
+            setmaxnreg_dec<LOW>();
         uint32_t stage = 0, phase = 0, filled_mask = 0, fill_parity = 0;
         bool skip = p.skip_first_load && blockIdx.x == 0;
         bool ok = true;
@@ -256,8 +255,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 mbar_arrive_expect_tx(fb, W_BYTES + SH::X_BYTES + 4 * TOK);
                 filled_mask |= 1u << stage;
                 fill_parity = (fill_parity & ~(1u << stage)) | (phase << stage);
-                tma_load_2d(w_dst, &tmW, kb * BK, (int32_t)i0, fb);
-                tma_load_2d(w_dst + W_BYTES / 2, &tmW, kb * BK, (int32_t)(p.I + i0), fb);
+                tma_load_3d(w_dst, &tmW, kb * BK, (int32_t)i0, 0, fb);  // gate rows, then up rows
                 tma_load_2d(sbase + SH::x_off + stage * SH::X_BYTES, &tmX, kb * BK, (int32_t)m0, fb);
                 tma_load_2d(slot, &tmS, (int32_t)m0, kb, fb);
                 cp_async4(slot + 4 * TOK, sw_gate + kb);
@@ -288,7 +286,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp == 1) {
         // ---------------------------------------------------------- MMA ----
         if constexpr (SH::REBALANCE)
-            setmaxnreg_dec<SH::LOW>();
+            setmaxnreg_dec<LOW>();
         constexpr uint32_t IDESC = TILING == FEW ? idesc_e4m3_f32(BI, TOK, false) : idesc_e4m3_f32(TOK, 2 * BI, false);
         bool ok = true, committed = false;
         uint32_t stage = 0, phase = 0, buf = 0, tphase = 0, last_buf = 0, last_par = 0;
@@ -354,13 +352,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         tmem_dealloc(tmem_base, SH::TMEM_COLS);
     } else if (warp < PROMO_WARP0) {
         if constexpr (SH::REBALANCE)
-            setmaxnreg_dec<SH::LOW>();  // completes warpgroup 0; no role
+            setmaxnreg_dec<LOW>();  // completes warpgroup 0; no role
         cluster_sync();
         cluster_sync();
     } else {
         // ---------------------------------------------------- promotion ----
         if constexpr (SH::REBALANCE)
-            setmaxnreg_inc<SH::HIGH>();
+            setmaxnreg_inc<HIGH>();
         const int quarter = warp & 3, half = (warp - PROMO_WARP0) >> 2;
         constexpr int SUMS = TILING == FEW ? TOK : BI;  // per thread
         float2 acc[SUMS / 2];
@@ -495,11 +493,8 @@ void launch_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&attr)[2], int6
 template <int TILING>
 bool set_attributes()
 {
-    auto k = gated_cluster_kernel<TILING>;
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<TILING>::total) == cudaSuccess)
-        return true;
-    cudaGetLastError();
-    return false;
+    static std::atomic<uint64_t> done{0};
+    return allow_smem(gated_cluster_kernel<TILING>, Shape<TILING>::total, done);
 }
 
 // Clusters of `split` CTAs that run at once. A cluster's CTAs share a GPC, so
@@ -541,8 +536,10 @@ int launch_clusters(const GatedArgs &g, int split, cudaStream_t s)
     p.wait_limit_ns = wait_limit_ns();
     p.skip_first_load = take_skip_first_load() ? 1 : 0;
     CUtensorMap tw, tx, ts;
+    const uint64_t dims[2] = {(uint64_t)g.I, 2}, strides[2] = {1, (uint64_t)g.I};
+    const uint32_t box[2] = {BI, 2};
     if (!p.status ||
-        !make_map(&tw, g.wq, (uint64_t)g.K, (uint64_t)(2 * g.I), (uint64_t)g.ldw, BK, BI) ||
+        !make_map_rows(&tw, g.wq, (uint64_t)g.K, (uint64_t)g.ldw, 2, dims, strides, BK, box) ||
         !make_map(&tx, g.xq, (uint64_t)g.K, (uint64_t)g.M, (uint64_t)g.ldx, BK, SH::TOK) ||
         !make_map_f32_row(&ts, g.sx, (uint64_t)g.M, (uint64_t)(g.K / BK), (uint64_t)g.ld_sx, SH::TOK))
         return FP8FG_ECUDA;
@@ -551,12 +548,17 @@ int launch_clusters(const GatedArgs &g, int split, cudaStream_t s)
         return FP8FG_ECUDA;
     if constexpr (SH::REBALANCE) {
         // the setmaxnreg split must fit in the registers the launch holds
-        cudaFuncAttributes fa;
-        if (cudaFuncGetAttributes(&fa, k) != cudaSuccess) {
-            cudaGetLastError();
-            return FP8FG_ECUDA;
+        // (asked once: the kernel has one binary)
+        static std::atomic<int> regs{0};
+        if (regs.load() == 0) {
+            cudaFuncAttributes fa;
+            if (cudaFuncGetAttributes(&fa, k) != cudaSuccess) {
+                cudaGetLastError();
+                return FP8FG_ECUDA;
+            }
+            regs.store(fa.numRegs);
         }
-        if (fa.numRegs < SH::LAUNCH_MIN)
+        if (regs.load() < LAUNCH_MIN)
             return FP8FG_EUNSUPPORTED;
     }
     cudaLaunchConfig_t cfg;
@@ -593,21 +595,24 @@ void consider(int64_t tiles, int64_t num_kb, double block_us, double fixed_us, d
 // The shortest estimate: waves x (contraction blocks of a CTA x time per block
 // + the fixed part of a tile + a term per CTA of the cluster). The constants
 // are fits to measured times (us, loads from DRAM): 24 tokens through K x 1024
-// with K = 1024 / 7168 and no split 7.7 / 29.1 (FEW); 333 tokens 10.8 / 29.4
-// (ROWS) and 8.7 / 31.8 (persistent, whose epilogue overlaps nothing but has
-// no cluster barriers). Measured against every other tiling and split for 1 to
-// 1024 tokens and widths of 128 to 18432, the choice was the fastest or within
-// 6 % of it: 333 tokens through 7168 x 2048 take 19.2 us split in two against
-// 31.8 us in persistent tiles, through 2048 x 8192 29.0 against 22.8.
+// with K = 1024 / 7168 and no split 7.7 / 29.1 (FEW); 333 tokens 10.6 / 28.6
+// (ROWS) and 8.5 / 29.1 (persistent, which has no cluster barriers). Measured
+// against every other tiling and split for 1 to 1500 tokens and widths of 128
+// to 18432, the choice was the fastest or within 5 % of it: 333 tokens through
+// 7168 x 2048 take 18.7 us split in two against 29.1 us in persistent tiles,
+// through 2048 x 8192 29.0 against 22.8.
 Plan choose(int64_t M, int64_t I, int64_t K)
 {
     const int64_t sms = sm_count() > 0 ? sm_count() : 1, num_kb = K / BK, cols = I / BI, rows = (M + 127) / 128;
     Plan best = {PERSISTENT, 1};
-    double best_us = (double)((rows * cols + sms - 1) / sms) * (num_kb * 0.48 + 4.9);
-    if (M <= Shape<FEW>::TOK)
+    double best_us = (double)((rows * cols + sms - 1) / sms) * (num_kb * 0.43 + 5.0);
+    if (M <= Shape<FEW>::TOK) {
+        // (always: wide weights are bound by the memory, which the estimates
+        // leave out; one token through 7168 x 18432: 43 us, persistent 58)
+        best_us = 1e30;
         consider<FEW>(cols, num_kb, 0.45, 4.1, 0.15, best, best_us);
-    else if (rows * cols <= sms)
-        consider<ROWS>(rows * cols, num_kb, 0.42, 7.2, 0.35, best, best_us);
+    } else if (rows * cols <= sms)
+        consider<ROWS>(rows * cols, num_kb, 0.38, 7.6, 0.35, best, best_us);
     return best;
 }
 

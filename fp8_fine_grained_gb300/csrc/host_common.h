@@ -2,6 +2,8 @@
 // status word, SM count, wait limit and argument checks.
 #pragma once
 
+#include <atomic>
+
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -37,6 +39,28 @@ inline int launch_status()
 {
     cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? FP8FG_OK : FP8FG_ECUDA;
+}
+
+// Allow `bytes` of dynamic shared memory, once per kernel and device: `done`
+// holds a bit per device and belongs to the kernel. (The call costs about as
+// much as the rest of a launch's preparation.)
+template <typename K>
+bool allow_smem(K k, size_t bytes, std::atomic<uint64_t> &done)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        cudaGetLastError();
+        return false;
+    }
+    const uint64_t bit = 1ull << dev;
+    if (done.load() & bit)
+        return true;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    done.fetch_or(bit);
+    return true;
 }
 
 // Launch with programmatic stream serialization: the grid may start while the

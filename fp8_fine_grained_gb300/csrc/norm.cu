@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(max_threads(W), min_ctas(W, false)) rmsnorm_fw
             if (ahead < p.T && !*wc.abort_flag)
                 fetch(ahead, ring.slot, ring.phase ^ 1);
         }
-        const float rstd = rsqrtf(ss / (float)p.D + p.eps);
+        const float rstd = __frsqrt_rn(ss / (float)p.D + p.eps);
         if (threadIdx.x == 0)
             p.rstd[t] = rstd;
         // the groups' maxima, then one division sequence for a half-warp's CPT
@@ -587,31 +587,31 @@ int ring_grid(int64_t T, const RingShape &r)
     return (int)(T < cap ? T : (cap > 0 ? cap : 1));
 }
 
-template <typename K, typename P>
-int launch_ring(K k, const P &p, int grid, int threads, size_t smem, cudaStream_t s)
+// (every instantiation may take all of a CTA's shared memory)
+template <auto K, typename P>
+int launch_ring(const P &p, int grid, int threads, size_t smem, cudaStream_t s)
 {
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
-        cudaGetLastError();
+    static std::atomic<uint64_t> done{0};
+    if (!allow_smem(K, 226 * 1024, done))
         return FP8FG_ECUDA;
-    }
-    return launch_pss(k, dim3((unsigned)grid), threads, smem, s, p);
+    return launch_pss(K, dim3((unsigned)grid), threads, smem, s, p);
 }
 
 template <int W>
 int launch_fwd(const NormFwd &p, int grid, int threads, size_t smem, bool p2, cudaStream_t s)
 {
     if (p.r)
-        return p2 ? launch_ring(rmsnorm_fwd_kernel<W, true, true>, p, grid, threads, smem, s)
-                  : launch_ring(rmsnorm_fwd_kernel<W, true, false>, p, grid, threads, smem, s);
-    return p2 ? launch_ring(rmsnorm_fwd_kernel<W, false, true>, p, grid, threads, smem, s)
-              : launch_ring(rmsnorm_fwd_kernel<W, false, false>, p, grid, threads, smem, s);
+        return p2 ? launch_ring<rmsnorm_fwd_kernel<W, true, true>>(p, grid, threads, smem, s)
+                  : launch_ring<rmsnorm_fwd_kernel<W, true, false>>(p, grid, threads, smem, s);
+    return p2 ? launch_ring<rmsnorm_fwd_kernel<W, false, true>>(p, grid, threads, smem, s)
+              : launch_ring<rmsnorm_fwd_kernel<W, false, false>>(p, grid, threads, smem, s);
 }
 
 template <int W>
 int launch_bwd(const NormBwd &p, int grid, int threads, size_t smem, cudaStream_t s)
 {
-    return p.dres ? launch_ring(rmsnorm_bwd_kernel<W, true>, p, grid, threads, smem, s)
-                  : launch_ring(rmsnorm_bwd_kernel<W, false>, p, grid, threads, smem, s);
+    return p.dres ? launch_ring<rmsnorm_bwd_kernel<W, true>>(p, grid, threads, smem, s)
+                  : launch_ring<rmsnorm_bwd_kernel<W, false>>(p, grid, threads, smem, s);
 }
 
 bool norm_width_ok(int64_t D) { return D >= 0 && D % GROUP == 0 && D <= NORM_MAX_D; }
