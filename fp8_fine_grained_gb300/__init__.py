@@ -836,32 +836,28 @@ def grad_clip(grads, max_norm, eps=1e-6, out=None, norm=None, stream=None):
         raise ValueError("out must hold one tensor per gradient")
     if not n:
         raise ValueError("grads must hold at least one tensor")
-    # one pass of C-level calls per attribute: with hundreds of tensors the
-    # lists are the cost of the call
+    # one pass of C-level calls per attribute over all tensors: with hundreds of
+    # them these lists are the cost of the call
     Tensor = torch.Tensor
     kind_of = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
-    types, sizes = list(map(attrgetter("dtype"), grads)), list(map(Tensor.numel, grads))
-    if not all(map(kind_of.__contains__, types)):
+    both = grads if out is None else grads + outs
+    types, sizes = list(map(attrgetter("dtype"), both)), list(map(Tensor.numel, both))
+    uniform = types.count(types[0]) == len(types)
+    if not all(t in kind_of for t in (types[:1] if uniform else set(types[:n]))):
         raise ValueError("gradients must be float32 or bfloat16")
-    if not all(map(Tensor.is_contiguous, grads)):
-        raise ValueError("gradients must be contiguous")
-    ptrs = array("q", map(Tensor.data_ptr, grads))
-    if out is None:
-        out_ptrs = ptrs
-    else:
-        if list(map(attrgetter("dtype"), outs)) != types or list(map(Tensor.numel, outs)) != sizes \
-                or not all(map(Tensor.is_contiguous, outs)):
-            raise ValueError("out must match the gradients' sizes and types and be contiguous")
-        out_ptrs = array("q", map(Tensor.data_ptr, outs))
+    if out is not None and (sizes[:n] != sizes[n:] or not (uniform or types[:n] == types[n:])):
+        raise ValueError("out must match the gradients' sizes and types")
+    if not all(map(Tensor.is_contiguous, both)):
+        raise ValueError("gradients and out must be contiguous")
     if norm is None:
         norm = torch.empty(2, dtype=torch.float32, device=grads[0].device)
     _vector(norm, torch.float32, 2, "norm")
-    is_cuda = attrgetter("is_cuda")
-    if not (norm.is_cuda and all(map(is_cuda, grads)) and (out is None or all(map(is_cuda, outs)))):
+    if not (norm.is_cuda and all(map(attrgetter("is_cuda"), both))):
         raise ValueError("grads, out and norm must be CUDA tensors")
+    ptrs = array("q", map(Tensor.data_ptr, both))
     table = array("q", bytes(32 * n))       # fp8fg_grad: g, out, n, kind (with its padding)
-    table[0::4], table[1::4], table[2::4] = ptrs, out_ptrs, array("q", sizes)
-    table[3::4] = array("q", map(kind_of.__getitem__, types))
+    table[0::4], table[1::4], table[2::4] = ptrs[:n], ptrs[-n:], array("q", sizes[:n])
+    table[3::4] = array("q", [kind_of[types[0]]]) * n if uniform else array("q", map(kind_of.get, types[:n]))
     L = lib()
     nbytes = L.fp8fg_grad_clip_workspace(n)
     ws = _workspace(nbytes, norm, stream)
