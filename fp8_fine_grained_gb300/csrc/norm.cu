@@ -94,6 +94,15 @@ __device__ __forceinline__ void load_gamma(const void *gamma, bool f32, int c, f
     }
 }
 
+// x^(-1/2) for x > 0: the hardware's approximation and one Newton step, within
+// an ulp (the correctly rounded intrinsic is 1 us slower over 8191 rows); an
+// overflowed sum of squares gives 0
+__device__ __forceinline__ float inv_sqrt(float x)
+{
+    const float r = rsqrtf(x);
+    return isinf(x) ? r : fmaf(0.5f * r, fmaf(-x * r, r, 1.0f), r);
+}
+
 __device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
 
 // Sum over the block in a fixed order. `part` holds one slot per warp and is
@@ -120,10 +129,23 @@ __device__ __forceinline__ float block_sum(float v, float *part, int nwarps)
 }
 
 // Dynamic shared memory: the ring, `slots` slots of `tensors` rows of D bf16
-// values each; one "row landed" barrier per slot; gamma (backward). Rows are the
+// values each; one "row landed" barrier per slot; gamma where it is staged. Rows are the
 // CTA's own: blockIdx, blockIdx + grid, ...
 constexpr int MAX_SLOTS = 8;
 constexpr uint32_t BAR_BYTES = 8 * MAX_SLOTS;
+
+// Where gamma is staged in shared memory: in the backward pass, which reads it
+// twice per row, and in the forward pass without a residual (8192 x 7168: 39 us,
+// from global memory 42). With a residual the loads from global memory are
+// moved over the reduction's barrier and the space serves the ring better (65
+// us, staged 72). The widest rows need the space for their second slot.
+constexpr bool stages_gamma(int w, bool bwd, int tensors) { return w != WIDE && (bwd || tensors == 1); }
+
+__device__ __forceinline__ void stage_gamma(uint8_t *dst, const void *gamma, uint32_t bytes)
+{
+    for (uint32_t i = threadIdx.x; i < bytes / 16; i += blockDim.x)
+        reinterpret_cast<uint4 *>(dst)[i] = static_cast<const uint4 *>(gamma)[i];
+}
 
 struct Ring {
     uint32_t base, bars, slot_bytes;
@@ -190,6 +212,9 @@ __global__ void __launch_bounds__(max_threads(W), min_ctas(W, false)) rmsnorm_fw
     const int nchunk = p.D / 8, nwarps = blockDim.x >> 5;
     const uint32_t row_bytes = 2 * (uint32_t)p.D;
     Ring ring{smem_u32(smem), smem_u32(smem) + p.slots * TENSORS * row_bytes, TENSORS * row_bytes, p.slots};
+    constexpr bool STAGED = stages_gamma(W, false, TENSORS);
+    uint8_t *const staged = smem + p.slots * TENSORS * row_bytes + BAR_BYTES;
+    const void *const gamma = STAGED ? staged : p.gamma;
     const WaitCtl wc{&abort_flag, p.status, p.wait_limit_ns};
     uint32_t pending = 0, parity = 0;  // thread 0: slots ever filled, parity of the last fill
     auto fetch = [&](int64_t t, int slot, uint32_t par) {
@@ -212,6 +237,8 @@ __global__ void __launch_bounds__(max_threads(W), min_ctas(W, false)) rmsnorm_fw
     if (threadIdx.x == 0)
         for (int s = 0; s < p.slots && blockIdx.x + (int64_t)s * gridDim.x < p.T; ++s)
             fetch(blockIdx.x + (int64_t)s * gridDim.x, s, 0);
+    if constexpr (STAGED)
+        stage_gamma(staged, p.gamma, p.gamma_f32 ? 4 * p.D : 2 * p.D);
     __syncthreads();
     int b = 0;
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, b ^= 1, ring.next()) {
@@ -245,7 +272,7 @@ __global__ void __launch_bounds__(max_threads(W), min_ctas(W, false)) rmsnorm_fw
             if (ahead < p.T && !*wc.abort_flag)
                 fetch(ahead, ring.slot, ring.phase ^ 1);
         }
-        const float rstd = __frsqrt_rn(ss / (float)p.D + p.eps);
+        const float rstd = inv_sqrt(ss / (float)p.D + p.eps);
         if (threadIdx.x == 0)
             p.rstd[t] = rstd;
         // the groups' maxima, then one division sequence for a half-warp's CPT
@@ -258,7 +285,7 @@ __global__ void __launch_bounds__(max_threads(W), min_ctas(W, false)) rmsnorm_fw
             const int c = threadIdx.x + i * blockDim.x;
             float2 g[4];
             unpack8(v[i], y[i]);
-            load_gamma(p.gamma, p.gamma_f32, c < nchunk ? c : 0, g);
+            load_gamma(gamma, p.gamma_f32, c < nchunk ? c : 0, g);
             float amax = 0.0f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -381,8 +408,9 @@ __global__ void __launch_bounds__(max_threads(W), min_ctas(W, true)) rmsnorm_bwd
     const int nchunk = p.D / 8, nwarps = blockDim.x >> 5;
     const uint32_t row_bytes = 2 * (uint32_t)p.D;
     Ring ring{smem_u32(smem), smem_u32(smem) + p.slots * TENSORS * row_bytes, TENSORS * row_bytes, p.slots};
+    constexpr bool STAGED = stages_gamma(W, true, TENSORS);
     uint8_t *const staged = smem + p.slots * TENSORS * row_bytes + BAR_BYTES;
-    const void *const gamma = W == WIDE ? p.gamma : staged;
+    const void *const gamma = STAGED ? staged : p.gamma;
     const WaitCtl wc{&abort_flag, p.status, p.wait_limit_ns};
     uint32_t pending = 0, parity = 0;
     auto fetch = [&](int64_t t, int slot, uint32_t par) {
@@ -406,11 +434,8 @@ __global__ void __launch_bounds__(max_threads(W), min_ctas(W, true)) rmsnorm_bwd
     if (threadIdx.x == 0)
         for (int s = 0; s < p.slots && blockIdx.x + (int64_t)s * gridDim.x < p.T; ++s)
             fetch(blockIdx.x + (int64_t)s * gridDim.x, s, 0);
-    // gamma is read twice per row: from global memory each row would wait for
-    // it again. (The widest rows need the space for their second slot.)
-    if constexpr (W != WIDE)
-        for (int i = threadIdx.x; i < (p.gamma_f32 ? p.D / 4 : p.D / 8); i += blockDim.x)
-            reinterpret_cast<uint4 *>(staged)[i] = static_cast<const uint4 *>(p.gamma)[i];
+    if constexpr (STAGED)
+        stage_gamma(staged, p.gamma, p.gamma_f32 ? 4 * p.D : 2 * p.D);
     __syncthreads();
     float2 dg[CPT][4];
 #pragma unroll
@@ -564,7 +589,7 @@ struct RingShape {
 RingShape ring_shape(int64_t D, int tensors, bool gamma_f32, bool bwd)
 {
     const RowShape rs = row_shape(D);
-    const int64_t gamma_bytes = bwd && rs.width != WIDE ? (gamma_f32 ? 4 * D : 2 * D) : 0;
+    const int64_t gamma_bytes = stages_gamma(rs.width, bwd, tensors) ? (gamma_f32 ? 4 * D : 2 * D) : 0;
     constexpr int64_t SM_BYTES = 226 * 1024;                      // of an SM
     const int64_t beside = gamma_bytes + BAR_BYTES + 1024 + 512;  // of a CTA beside the ring, 1 KB of it the system's
     const int64_t slot = 2 * D * tensors;
