@@ -23,8 +23,6 @@ plus the convenience wrappers fprop / dgrad / wgrad and device_status().
 """
 import ctypes
 import os
-from array import array
-from operator import attrgetter
 
 FPROP, DGRAD, WGRAD = 0, 1, 2
 OUT_F32, OUT_BF16 = 0, 1
@@ -32,6 +30,7 @@ OUT_F32, OUT_BF16 = 0, 1
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfp8fg.so")
 _lib = None
+_helper = None
 
 
 class Fp8fgError(RuntimeError):
@@ -92,6 +91,21 @@ def lib():
             getattr(L, f).restype = I32
         _lib = L
     return _lib
+
+
+def _tensor_list():
+    """The helper module that reads lists of tensors (raises if it has not been
+    built); it links against torch, so torch comes first."""
+    global _helper
+    if _helper is None:
+        _torch()
+        try:
+            from . import _tensors as m
+        except ImportError as e:
+            raise RuntimeError("_tensors.so is not built for this machine (%s); run `python "
+                               "fp8_fine_grained_gb300/build.py` (or __graft_entry__.build()) first" % e)
+        _helper = m
+    return _helper
 
 
 def status_str(code):
@@ -590,7 +604,9 @@ def fp8_moe_combine(y, dest, w, out_dtype=None, out=None, stream=None):
 # ------------------------------------------- between a gated MLP's GEMMs ----
 # These calls are short (a decoding step spends more time here than on the
 # GPU), so each tensor is looked at once: _matrix and _vector check it and
-# return what the library needs.
+# return what the library needs. With a stream of its own a call runs wholly
+# under it: outputs and scratch that the call allocates come from that stream's
+# memory, so that no work still queued on the current stream can be using it.
 
 def _matrix(t, dtype, rows, cols, name):
     """Row pitch of a 2-D row-major tensor of the dtype that covers [rows, cols]."""
@@ -617,14 +633,9 @@ def _gamma_kind(gamma, D):
     return _out_code(gamma.dtype)
 
 
-def _workspace(nbytes, like, stream):
-    """Scratch of one call, allocated on the current stream; another stream
-    that uses it is recorded, so that the memory is not handed out while that
-    stream still runs."""
-    w = _torch().empty(nbytes, dtype=_torch().uint8, device=like.device)
-    if stream is not None and w.is_cuda:
-        w.record_stream(stream)
-    return w
+def _under(stream, fn, *args, **kw):
+    with _torch().cuda.stream(stream):
+        return fn(*args, **kw)
 
 
 def fp8_rmsnorm(x, gamma, eps=1e-6, residual=None, h=None, q=None, scales=None, rstd=None, stream=None, pow2=False):
@@ -636,6 +647,8 @@ def fp8_rmsnorm(x, gamma, eps=1e-6, residual=None, h=None, q=None, scales=None, 
     float32. Returns (q uint8 [T, D], scales float32 [D/128, ld_s>=T], h,
     rstd float32 [T]); h and rstd are what fp8_rmsnorm_bwd needs. h may be x
     or residual (in place)."""
+    if stream is not None:
+        return _under(stream, fp8_rmsnorm, x, gamma, eps, residual, h, q, scales, rstd, None, pow2)
     torch = _torch()
     bf16, f32, u8 = torch.bfloat16, torch.float32, torch.uint8
     ldx = _matrix(x, bf16, 0, 0, "x")
@@ -666,7 +679,7 @@ def fp8_rmsnorm(x, gamma, eps=1e-6, residual=None, h=None, q=None, scales=None, 
         _on_gpu((x, "x"), (gamma, "gamma"), (residual, "residual"), (h, "h"), (q, "q"), (scales, "scales"),
                 (rstd, "rstd"))
     rc = lib().fp8_rmsnorm(x.data_ptr(), ldx, pr, ldr, gamma.data_ptr(), kind, T, D, eps, ph, ldh, q.data_ptr(), ldq,
-                           scales.data_ptr(), lds, rstd.data_ptr(), 1 if pow2 else 0, _stream(stream))
+                           scales.data_ptr(), lds, rstd.data_ptr(), 1 if pow2 else 0, _stream(None))
     if rc:
         _check(rc, "fp8_rmsnorm")
     return q, scales, x if h is None else h, rstd
@@ -676,6 +689,8 @@ def fp8_rmsnorm_t(h, rstd, gamma, qT=None, scalesT=None, stream=None, pow2=False
     """The norm's output of fp8_rmsnorm, recomputed from h [T, D] and rstd, as
     fp8_quant_1x128(..., transpose=True) lays it out (T % 128 == 0): qT uint8
     [D, T], scalesT float32 [T/128, ld_s>=D]."""
+    if stream is not None:
+        return _under(stream, fp8_rmsnorm_t, h, rstd, gamma, qT, scalesT, None, pow2)
     torch = _torch()
     f32, u8 = torch.float32, torch.uint8
     ldh = _matrix(h, torch.bfloat16, 0, 0, "h")
@@ -690,7 +705,7 @@ def fp8_rmsnorm_t(h, rstd, gamma, qT=None, scalesT=None, stream=None, pow2=False
     lds = _matrix(scalesT, f32, T // 128, D, "scalesT")
     _on_gpu((h, "h"), (rstd, "rstd"), (gamma, "gamma"), (qT, "qT"), (scalesT, "scalesT"))
     rc = lib().fp8_rmsnorm_t(h.data_ptr(), ldh, rstd.data_ptr(), gamma.data_ptr(), kind, T, D, qT.data_ptr(), ldq,
-                             scalesT.data_ptr(), lds, 1 if pow2 else 0, _stream(stream))
+                             scalesT.data_ptr(), lds, 1 if pow2 else 0, _stream(None))
     if rc:
         _check(rc, "fp8_rmsnorm_t")
     return qT, scalesT
@@ -702,6 +717,8 @@ def fp8_rmsnorm_bwd(dy, h, rstd, gamma, dres=None, dx=None, dgamma=None, stream=
     gradient that reaches h on the residual stream. Returns (dx bf16 [T, D],
     dgamma float32 [D]); dx is the gradient of x and of the residual alike.
     dx may be dy or dres (in place)."""
+    if stream is not None:
+        return _under(stream, fp8_rmsnorm_bwd, dy, h, rstd, gamma, dres, dx, dgamma)
     torch = _torch()
     bf16, f32 = torch.bfloat16, torch.float32
     lddy = _matrix(dy, bf16, 0, 0, "dy")
@@ -724,10 +741,10 @@ def fp8_rmsnorm_bwd(dy, h, rstd, gamma, dres=None, dx=None, dgamma=None, stream=
                 (dgamma, "dgamma"))
     L = lib()
     nbytes = L.fp8_rmsnorm_bwd_workspace(T, D)
-    ws = _workspace(nbytes, dy, stream)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dy.device)
     rc = L.fp8_rmsnorm_bwd(dy.data_ptr(), lddy, h.data_ptr(), ldh, rstd.data_ptr(), gamma.data_ptr(), kind, pdres,
                            lddres, T, D, dx.data_ptr(), lddx, dgamma.data_ptr(), ws.data_ptr(), nbytes,
-                           _stream(stream))
+                           _stream(None))
     if rc:
         _check(rc, "fp8_rmsnorm_bwd")
     return dx, dgamma
@@ -742,6 +759,8 @@ def fp8_gated_gemm(xq, sx, wq, sw, h=None, scales=None, gu=None, save=False, str
     float32 [I/128, ld_s>=M], gu): h quantised 1x128 for the down projection,
     gu the two projections in bf16 [M, 2I] for fp8_gated_bwd (None unless
     save=True or a gu buffer is given)."""
+    if stream is not None:
+        return _under(stream, fp8_gated_gemm, xq, sx, wq, sw, h, scales, gu, save, None, pow2)
     torch = _torch()
     f32, u8 = torch.float32, torch.uint8
     ldx = _matrix(xq, u8, 0, 0, "xq")
@@ -771,7 +790,7 @@ def fp8_gated_gemm(xq, sx, wq, sw, h=None, scales=None, gu=None, save=False, str
             and (gu is None or gu.is_cuda)):
         _on_gpu((xq, "xq"), (sx, "sx"), (wq, "wq"), (sw, "sw"), (h, "h"), (scales, "scales"), (gu, "gu"))
     rc = lib().fp8_gated_gemm(xq.data_ptr(), sx.data_ptr(), ldx, ldsx, wq.data_ptr(), sw.data_ptr(), ldw, M, I, K,
-                              h.data_ptr(), ldh, scales.data_ptr(), lds, pgu, ldgu, 1 if pow2 else 0, _stream(stream))
+                              h.data_ptr(), ldh, scales.data_ptr(), lds, pgu, ldgu, 1 if pow2 else 0, _stream(None))
     if rc:
         _check(rc, "fp8_gated_gemm")
     return h, scales, gu
@@ -785,6 +804,8 @@ def fp8_gated_bwd(gu, dh, q=None, scales=None, qT=None, scalesT=None, hqT=None, 
     per column (qT [2I, M], scalesT [M/128, >=2I]: wgrad operand), and the
     recomputed h per column (hqT [I, M], hscalesT [M/128, >=I]: the down
     projection's wgrad operand)."""
+    if stream is not None:
+        return _under(stream, fp8_gated_bwd, gu, dh, q, scales, qT, scalesT, hqT, hscalesT, None, pow2)
     torch = _torch()
     u8, f32, bf16 = torch.uint8, torch.float32, torch.bfloat16
     ldgu = _matrix(gu, bf16, 0, 0, "gu")
@@ -814,7 +835,7 @@ def fp8_gated_bwd(gu, dh, q=None, scales=None, qT=None, scalesT=None, hqT=None, 
                 (hscalesT, "hscalesT"))
     rc = lib().fp8_gated_bwd(gu.data_ptr(), ldgu, dh.data_ptr(), lddh, M, I, q.data_ptr(), ldq, scales.data_ptr(), lds,
                              qT.data_ptr(), ldqT, scalesT.data_ptr(), ldsT, hqT.data_ptr(), ldhT, hscalesT.data_ptr(),
-                             ldhs, 1 if pow2 else 0, _stream(stream))
+                             ldhs, 1 if pow2 else 0, _stream(None))
     if rc:
         _check(rc, "fp8_gated_bwd")
     return q, scales, qT, scalesT, hqT, hscalesT
@@ -828,6 +849,8 @@ def grad_clip(grads, max_norm, eps=1e-6, out=None, norm=None, stream=None):
     (default: the gradients themselves). Returns (norm, out): norm float32 [2]
     on the device holds the norm before scaling and the factor min(1, max_norm
     / (norm + eps)); nothing is copied to the host."""
+    if stream is not None:
+        return _under(stream, grad_clip, grads, max_norm, eps, out, norm)
     torch = _torch()
     grads = list(grads)
     outs = grads if out is None else list(out)
@@ -836,33 +859,17 @@ def grad_clip(grads, max_norm, eps=1e-6, out=None, norm=None, stream=None):
         raise ValueError("out must hold one tensor per gradient")
     if not n:
         raise ValueError("grads must hold at least one tensor")
-    # one pass of C-level calls per attribute over all tensors: with hundreds of
-    # them these lists are the cost of the call
-    Tensor = torch.Tensor
-    kind_of = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
-    both = grads if out is None else grads + outs
-    types, sizes = list(map(attrgetter("dtype"), both)), list(map(Tensor.numel, both))
-    uniform = types.count(types[0]) == len(types)
-    if not all(t in kind_of for t in (types[:1] if uniform else set(types[:n]))):
-        raise ValueError("gradients must be float32 or bfloat16")
-    if out is not None and (sizes[:n] != sizes[n:] or not (uniform or types[:n] == types[n:])):
-        raise ValueError("out must match the gradients' sizes and types")
-    if not all(map(Tensor.is_contiguous, both)):
-        raise ValueError("gradients and out must be contiguous")
+    table = _tensor_list().describe(grads, outs)
     if norm is None:
         norm = torch.empty(2, dtype=torch.float32, device=grads[0].device)
     _vector(norm, torch.float32, 2, "norm")
-    if not (norm.is_cuda and all(map(attrgetter("is_cuda"), both))):
-        raise ValueError("grads, out and norm must be CUDA tensors")
-    ptrs = array("q", map(Tensor.data_ptr, both))
-    table = array("q", bytes(32 * n))       # fp8fg_grad: g, out, n, kind (with its padding)
-    table[0::4], table[1::4], table[2::4] = ptrs[:n], ptrs[-n:], array("q", sizes[:n])
-    table[3::4] = array("q", [kind_of[types[0]]]) * n if uniform else array("q", map(kind_of.get, types[:n]))
+    if norm.device != grads[0].device:
+        raise ValueError("norm must be on the gradients' device")
     L = lib()
     nbytes = L.fp8fg_grad_clip_workspace(n)
-    ws = _workspace(nbytes, norm, stream)
-    rc = L.fp8fg_grad_clip(table.buffer_info()[0], n, max_norm, eps, norm.data_ptr(), ws.data_ptr(), nbytes,
-                           _stream(stream))
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=norm.device)
+    rc = L.fp8fg_grad_clip(table, n, max_norm, eps, norm.data_ptr(), ws.data_ptr(), nbytes,
+                           _stream(None))
     if rc:
         _check(rc, "fp8fg_grad_clip")
     return norm, outs

@@ -1,12 +1,17 @@
-"""Build libfp8fg.so (the C-ABI library) in-tree with nvcc for sm_103a.
+"""Build libfp8fg.so (the C-ABI library) in-tree with nvcc for sm_103a, and the
+binding's CPython helper _tensors.so with the host compiler.
 
-Each CUDA translation unit compiles in parallel; the objects link into one
+Each translation unit compiles in parallel; the CUDA objects link into one
 shared library with the CUDA runtime linked statically, so the library loads
-on a machine without a GPU driver (nothing runs until a call is made).
+on a machine without a GPU driver (nothing runs until a call is made). The
+helper reads the metadata of torch tensors and is compiled against the
+installed torch.
 """
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -15,6 +20,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfp8fg.so")
+HELPER = os.path.join(HERE, "_tensors.so")
+HELPER_SOURCE = os.path.join(CSRC, "tensor_list.cpp")
 SOURCES = ["capi.cu", "quant.cu", "gemm.cu", "gemm_mx.cu", "moe.cu", "norm.cu", "gemm_gated.cu", "gated_bwd.cu",
            "clip.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -30,12 +37,41 @@ def nvcc():
 
 
 def _deps():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if not f.endswith(".cpp")]
     files.append(os.path.join(INCLUDE, "fp8fg.h"))
     return max(os.path.getmtime(f) for f in files)
 
 
+def helper_command(out):
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    inc, lib = os.path.join(torch, "include"), os.path.join(torch, "lib")
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-I", INCLUDE,
+            "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem",
+            sysconfig.get_paths()["include"], HELPER_SOURCE, "-o", out, "-L", lib, "-Wl,-rpath," + lib,
+            "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10"]
+
+
+def build_helper(force=False):
+    newest = max(os.path.getmtime(f) for f in (HELPER_SOURCE, os.path.join(INCLUDE, "fp8fg.h")))
+    if not force and os.path.exists(HELPER) and os.path.getmtime(HELPER) >= newest:
+        return HELPER
+    tmp = HELPER + ".tmp.%d" % os.getpid()
+    r = subprocess.run(helper_command(tmp), capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("%s failed:\n%s\n%s" % (HELPER_SOURCE, r.stdout, r.stderr))
+    os.replace(tmp, HELPER)
+    return HELPER
+
+
 def build(force=False, verbose=False, extra=()):
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        helper = ex.submit(build_helper, force)
+        lib = build_lib(force, verbose, extra)
+        helper.result()
+    return lib
+
+
+def build_lib(force=False, verbose=False, extra=()):
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps():
         return LIB
     os.makedirs(BUILD, exist_ok=True)

@@ -145,3 +145,16 @@ def test_repeatable_and_on_another_stream():
     got = fg.grad_clip(grads, 1.0, EPS, out=[torch.empty_like(g) for g in grads], stream=side)
     side.synchronize()
     assert torch.equal(want[0], got[0]) and all(torch.equal(a, b) for a, b in zip(want[1], got[1]))
+
+
+def test_table_rows_of_views():
+    """What the helper reads from views, several types and empty tensors."""
+    import struct
+    from fp8_fine_grained_gb300 import _tensors
+    flat, out = _grads([100], [F], seed=1)[0], torch.empty(100, device=DEV)
+    b = torch.zeros(3, 0, dtype=B, device=DEV)
+    rows = struct.unpack("<" + "qqqii" * 3, _tensors.describe([flat[3:10], b, flat[10:].view(9, 10)],
+                                                         [out[5:12], b, out[10:].view(90)]))
+    assert rows[0:5] == (flat.data_ptr() + 12, out.data_ptr() + 20, 7, 0, 0)
+    assert rows[7:10] == (0, 1, 0)
+    assert rows[10:15] == (flat.data_ptr() + 40, out.data_ptr() + 40, 90, 0, 0)

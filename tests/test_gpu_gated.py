@@ -58,7 +58,8 @@ def _check_fwd(ops, out, rows=None, pow2=False):
 
 @pytest.mark.parametrize("M,K,I", [(1, 128, 128), (1, 1024, 384), (3, 384, 128), (17, 7168, 256), (32, 512, 2048),
                                    (33, 256, 640), (64, 2048, 256), (65, 1152, 384), (128, 512, 512), (129, 256, 256),
-                                   (200, 640, 1152), (333, 1280, 384), (500, 384, 640)])
+                                   (200, 640, 1152), (333, 1280, 384), (500, 384, 640),
+                                   (2600, 256, 1024), (1537, 128, 1664)])
 @pytest.mark.parametrize("save", [False, True])
 def test_forward(M, K, I, save):
     ops = _operands(M, K, I, seed=M + K + I)
@@ -68,9 +69,9 @@ def test_forward(M, K, I, save):
     _check_fwd(ops, out)
 
 
-@pytest.mark.parametrize("M", [2, 40, 300])
-def test_forward_pow2(M):
-    ops = _operands(M, 512, 384, seed=3)
+@pytest.mark.parametrize("M,I", [(2, 384), (40, 384), (300, 384), (1300, 2048)])
+def test_forward_pow2(M, I):
+    ops = _operands(M, 512, I, seed=3)
     _check_fwd(ops, fg.fp8_gated_gemm(*ops, pow2=True), pow2=True)
 
 
@@ -83,10 +84,10 @@ def test_forward_workload_widths(M, K, I):
     assert fg.device_status() == 0
 
 
-@pytest.mark.parametrize("M", [5, 40, 150])
-def test_saturated_gates_and_zero_rows(M):
+@pytest.mark.parametrize("M,I", [(5, 256), (40, 256), (150, 256), (1500, 1792)])
+def test_saturated_gates_and_zero_rows(M, I):
     """Gates far out on both sides, and rows of zeros (scale 1, zero codes)."""
-    xq, sx, wq, sw = _operands(M, 256, 256, seed=8, wscale=1.0)
+    xq, sx, wq, sw = _operands(M, 256, I, seed=8, wscale=1.0)
     sx = sx.clone()
     sx[:, 1] *= 2.0 ** 12
     sx[:, 2] *= 2.0 ** -40
@@ -98,9 +99,9 @@ def test_saturated_gates_and_zero_rows(M):
     _check_fwd((xq, sx, wq, sw), out)
 
 
-@pytest.mark.parametrize("M", [7, 50, 139])
-def test_strides_and_untouched_padding(M):
-    K, I = 384, 256
+@pytest.mark.parametrize("M,I", [(7, 256), (50, 256), (139, 256), (1411, 1792)])
+def test_strides_and_untouched_padding(M, I):
+    K = 384
     xq, sx, wq, sw = _operands(M, K, I, seed=11)
     xp = torch.zeros(M, K + 64, dtype=torch.uint8, device=DEV)
     xp[:, 32:32 + K] = xq
@@ -122,9 +123,9 @@ def test_strides_and_untouched_padding(M):
     assert torch.equal(plain[0], hv) and torch.equal(plain[2], guv) and torch.equal(plain[1][:, :M], s[:, :M])
 
 
-@pytest.mark.parametrize("M", [1, 40, 200])
-def test_forward_is_repeatable(M):
-    ops = _operands(M, 2048, 512, seed=12)
+@pytest.mark.parametrize("M,I", [(1, 512), (40, 512), (200, 512), (1300, 2048)])
+def test_forward_is_repeatable(M, I):
+    ops = _operands(M, 2048, I, seed=12)
     a, b = fg.fp8_gated_gemm(*ops, save=True), fg.fp8_gated_gemm(*ops, save=True)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1][:, :M], b[1][:, :M]) and torch.equal(a[2], b[2])
 
@@ -136,11 +137,11 @@ def test_no_rows():
     assert fg.device_status() == 0
 
 
-@pytest.mark.parametrize("M", [8, 300])
-def test_forward_reports_a_withheld_load(M):
+@pytest.mark.parametrize("M,I", [(8, 256), (300, 256), (1300, 2048)])
+def test_forward_reports_a_withheld_load(M, I):
     """A load that never lands: the bounded waits run out, the status word
     says so and the next launch is clean."""
-    ops = _operands(M, 1024, 256, seed=14)
+    ops = _operands(M, 1024, I, seed=14)
     fg.set_wait_limit_ns(50_000_000)
     try:
         fg.inject_skip_first_load()
@@ -154,13 +155,20 @@ def test_forward_reports_a_withheld_load(M):
 
 
 def test_on_another_stream():
+    """A side stream's outputs come from its own memory: nothing that is queued
+    on the current stream can still be using it."""
     ops = _operands(100, 1024, 512, seed=15)
-    want = fg.fp8_gated_gemm(*ops)
+    gu, dh = _bwd_inputs(128, 256, seed=15)
+    want, wantb = fg.fp8_gated_gemm(*ops), fg.fp8_gated_bwd(gu, dh)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
-    got = fg.fp8_gated_gemm(*ops, stream=side)
+    junk = [torch.full((100, 512), 7, dtype=torch.uint8, device=DEV) for _ in range(20)]
+    del junk
+    got, gotb = fg.fp8_gated_gemm(*ops, stream=side), fg.fp8_gated_bwd(gu, dh, stream=side)
     side.synchronize()
     assert torch.equal(want[0], got[0]) and torch.equal(want[1][:, :100], got[1][:, :100])
+    assert all(torch.equal(a, b) for a, b in zip(wantb, gotb))
+    assert torch.cuda.current_stream() != side
 
 
 # ---------------------------------------------------------------- backward ----

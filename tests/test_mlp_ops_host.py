@@ -249,3 +249,22 @@ def test_code_check_finds_wrong_codes_and_scales():
     off[1, 1] *= 1.001
     with pytest.raises(AssertionError, match="scale"):
         R.check_codes(codes, off, ref, 0.0)
+
+
+def test_tensor_table():
+    """The rows that the helper writes, read back as the C structure, and its
+    refusals (the device is looked at last)."""
+    from fp8_fine_grained_gb300 import _tensors
+    flat = torch.arange(20, dtype=F32)
+    with pytest.raises(ValueError, match="CUDA"):
+        _tensors.describe([flat], [flat])
+    for args in ((), ([],), ([flat], (flat,)), ([flat], [])):
+        with pytest.raises(ValueError, match="two lists"):
+            _tensors.describe(*args)
+    with pytest.raises(ValueError, match="hold tensors"):
+        _tensors.describe([flat, 3], [flat, flat])
+    with pytest.raises(ValueError, match="contiguous"):
+        _tensors.describe([flat.to_sparse()], [flat])
+    with pytest.raises(ValueError, match="contiguous"):
+        _tensors.describe([flat[::2]], [flat[:10]])
+    assert _tensors.describe([], []) == b""
