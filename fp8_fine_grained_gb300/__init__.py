@@ -93,9 +93,9 @@ def lib():
     return _lib
 
 
-def _tensor_list():
-    """The helper module that reads lists of tensors (raises if it has not been
-    built); it links against torch, so torch comes first."""
+def _checks():
+    """The compiled helper that reads tensors' metadata (raises if it has not
+    been built); it links against torch, so torch comes first."""
     global _helper
     if _helper is None:
         _torch()
@@ -603,34 +603,19 @@ def fp8_moe_combine(y, dest, w, out_dtype=None, out=None, stream=None):
 
 # ------------------------------------------- between a gated MLP's GEMMs ----
 # These calls are short (a decoding step spends more time here than on the
-# GPU), so each tensor is looked at once: _matrix and _vector check it and
-# return what the library needs. With a stream of its own a call runs wholly
-# under it: outputs and scratch that the call allocates come from that stream's
-# memory, so that no work still queued on the current stream can be using it.
+# GPU), so the tensors are checked in the compiled helper: matrix (type, layout,
+# extent; returns the row pitch), vector, and on_gpu last. With a stream of its
+# own a call runs wholly under it: outputs and scratch that the call allocates
+# come from that stream's memory, so that no work still queued on the current
+# stream can be using it.
 
-def _matrix(t, dtype, rows, cols, name):
-    """Row pitch of a 2-D row-major tensor of the dtype that covers [rows, cols]."""
-    if t.dtype is not dtype:
-        _dtype(t, dtype, name)
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 2 or stride[1] != 1:
-        _layout(t, name)
-    if shape[0] < rows or shape[1] < cols:
-        _at_least(t, rows, cols, name)
-    return stride[0]
-
-
-def _vector(t, dtype, n, name):
-    if t.dtype is not dtype:
-        _dtype(t, dtype, name)
-    if t.dim() != 1 or t.numel() < n or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous vector of at least %d entries" % (name, n))
-
-
-def _gamma_kind(gamma, D):
-    if gamma.dim() != 1 or gamma.numel() != D or not gamma.is_contiguous():
-        raise ValueError("gamma must be a contiguous vector of %d entries" % D)
-    return _out_code(gamma.dtype)
+def _gamma_kind(H, gamma, D):
+    """OUT_BF16 or OUT_F32 of a norm's weight of D entries."""
+    kind = _out_code(gamma.dtype)
+    H.vector(gamma, gamma.dtype, D, "gamma")
+    if gamma.shape[0] != D:
+        raise ValueError("gamma must hold %d entries, got %d" % (D, gamma.shape[0]))
+    return kind
 
 
 def _under(stream, fn, *args, **kw):
@@ -649,19 +634,19 @@ def fp8_rmsnorm(x, gamma, eps=1e-6, residual=None, h=None, q=None, scales=None, 
     or residual (in place)."""
     if stream is not None:
         return _under(stream, fp8_rmsnorm, x, gamma, eps, residual, h, q, scales, rstd, None, pow2)
-    torch = _torch()
+    torch, H = _torch(), _checks()
     bf16, f32, u8 = torch.bfloat16, torch.float32, torch.uint8
-    ldx = _matrix(x, bf16, 0, 0, "x")
+    ldx = H.matrix(x, bf16, 0, 0, "x")
     T, D = x.shape
-    kind = _gamma_kind(gamma, D)
+    kind = _gamma_kind(H, gamma, D)
     ldr = ldh = pr = ph = 0
     if residual is not None:
-        ldr = _matrix(residual, bf16, T, D, "residual")
+        ldr = H.matrix(residual, bf16, T, D, "residual")
         if residual.shape != x.shape:
             raise ValueError("residual must be [%d, %d], got %s" % (T, D, tuple(residual.shape)))
         if h is None:
             h = torch.empty((T, D), dtype=bf16, device=x.device)
-        ldh = _matrix(h, bf16, T, D, "h")
+        ldh = H.matrix(h, bf16, T, D, "h")
         pr, ph = residual.data_ptr(), h.data_ptr()
     elif h is not None:
         raise ValueError("h is written only with a residual")
@@ -671,13 +656,10 @@ def fp8_rmsnorm(x, gamma, eps=1e-6, residual=None, h=None, q=None, scales=None, 
         scales = torch.empty((D // 128, _pad(max(T, 1), 4)), dtype=f32, device=x.device)
     if rstd is None:
         rstd = torch.empty(T, dtype=f32, device=x.device)
-    ldq = _matrix(q, u8, T, D, "q")
-    lds = _matrix(scales, f32, D // 128, T, "scales")
-    _vector(rstd, f32, T, "rstd")
-    if not (x.is_cuda and gamma.is_cuda and q.is_cuda and scales.is_cuda and rstd.is_cuda
-            and (residual is None or (residual.is_cuda and h.is_cuda))):
-        _on_gpu((x, "x"), (gamma, "gamma"), (residual, "residual"), (h, "h"), (q, "q"), (scales, "scales"),
-                (rstd, "rstd"))
+    ldq = H.matrix(q, u8, T, D, "q")
+    lds = H.matrix(scales, f32, D // 128, T, "scales")
+    H.vector(rstd, f32, T, "rstd")
+    H.on_gpu(x, "x", gamma, "gamma", residual, "residual", h, "h", q, "q", scales, "scales", rstd, "rstd")
     rc = lib().fp8_rmsnorm(x.data_ptr(), ldx, pr, ldr, gamma.data_ptr(), kind, T, D, eps, ph, ldh, q.data_ptr(), ldq,
                            scales.data_ptr(), lds, rstd.data_ptr(), 1 if pow2 else 0, _stream(None))
     if rc:
@@ -691,19 +673,19 @@ def fp8_rmsnorm_t(h, rstd, gamma, qT=None, scalesT=None, stream=None, pow2=False
     [D, T], scalesT float32 [T/128, ld_s>=D]."""
     if stream is not None:
         return _under(stream, fp8_rmsnorm_t, h, rstd, gamma, qT, scalesT, None, pow2)
-    torch = _torch()
+    torch, H = _torch(), _checks()
     f32, u8 = torch.float32, torch.uint8
-    ldh = _matrix(h, torch.bfloat16, 0, 0, "h")
+    ldh = H.matrix(h, torch.bfloat16, 0, 0, "h")
     T, D = h.shape
-    kind = _gamma_kind(gamma, D)
-    _vector(rstd, f32, T, "rstd")
+    kind = _gamma_kind(H, gamma, D)
+    H.vector(rstd, f32, T, "rstd")
     if qT is None:
         qT = torch.empty((D, T), dtype=u8, device=h.device)
     if scalesT is None:
         scalesT = torch.empty((T // 128, _pad(max(D, 1), 4)), dtype=f32, device=h.device)
-    ldq = _matrix(qT, u8, D, T, "qT")
-    lds = _matrix(scalesT, f32, T // 128, D, "scalesT")
-    _on_gpu((h, "h"), (rstd, "rstd"), (gamma, "gamma"), (qT, "qT"), (scalesT, "scalesT"))
+    ldq = H.matrix(qT, u8, D, T, "qT")
+    lds = H.matrix(scalesT, f32, T // 128, D, "scalesT")
+    H.on_gpu(h, "h", rstd, "rstd", gamma, "gamma", qT, "qT", scalesT, "scalesT")
     rc = lib().fp8_rmsnorm_t(h.data_ptr(), ldh, rstd.data_ptr(), gamma.data_ptr(), kind, T, D, qT.data_ptr(), ldq,
                              scalesT.data_ptr(), lds, 1 if pow2 else 0, _stream(None))
     if rc:
@@ -719,26 +701,23 @@ def fp8_rmsnorm_bwd(dy, h, rstd, gamma, dres=None, dx=None, dgamma=None, stream=
     dx may be dy or dres (in place)."""
     if stream is not None:
         return _under(stream, fp8_rmsnorm_bwd, dy, h, rstd, gamma, dres, dx, dgamma)
-    torch = _torch()
+    torch, H = _torch(), _checks()
     bf16, f32 = torch.bfloat16, torch.float32
-    lddy = _matrix(dy, bf16, 0, 0, "dy")
+    lddy = H.matrix(dy, bf16, 0, 0, "dy")
     T, D = dy.shape
-    ldh = _matrix(h, bf16, T, D, "h")
-    _vector(rstd, f32, T, "rstd")
-    kind = _gamma_kind(gamma, D)
+    ldh = H.matrix(h, bf16, T, D, "h")
+    H.vector(rstd, f32, T, "rstd")
+    kind = _gamma_kind(H, gamma, D)
     lddres = pdres = 0
     if dres is not None:
-        lddres, pdres = _matrix(dres, bf16, T, D, "dres"), dres.data_ptr()
+        lddres, pdres = H.matrix(dres, bf16, T, D, "dres"), dres.data_ptr()
     if dx is None:
         dx = torch.empty((T, D), dtype=bf16, device=dy.device)
     if dgamma is None:
         dgamma = torch.empty(D, dtype=f32, device=dy.device)
-    lddx = _matrix(dx, bf16, T, D, "dx")
-    _vector(dgamma, f32, D, "dgamma")
-    if not (dy.is_cuda and h.is_cuda and rstd.is_cuda and gamma.is_cuda and dx.is_cuda and dgamma.is_cuda
-            and (dres is None or dres.is_cuda)):
-        _on_gpu((dy, "dy"), (h, "h"), (rstd, "rstd"), (gamma, "gamma"), (dres, "dres"), (dx, "dx"),
-                (dgamma, "dgamma"))
+    lddx = H.matrix(dx, bf16, T, D, "dx")
+    H.vector(dgamma, f32, D, "dgamma")
+    H.on_gpu(dy, "dy", h, "h", rstd, "rstd", gamma, "gamma", dres, "dres", dx, "dx", dgamma, "dgamma")
     L = lib()
     nbytes = L.fp8_rmsnorm_bwd_workspace(T, D)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dy.device)
@@ -761,12 +740,12 @@ def fp8_gated_gemm(xq, sx, wq, sw, h=None, scales=None, gu=None, save=False, str
     save=True or a gu buffer is given)."""
     if stream is not None:
         return _under(stream, fp8_gated_gemm, xq, sx, wq, sw, h, scales, gu, save, None, pow2)
-    torch = _torch()
+    torch, H = _torch(), _checks()
     f32, u8 = torch.float32, torch.uint8
-    ldx = _matrix(xq, u8, 0, 0, "xq")
+    ldx = H.matrix(xq, u8, 0, 0, "xq")
     M, K = xq.shape
-    ldsx = _matrix(sx, f32, K // 128, M, "sx")
-    ldw = _matrix(wq, u8, 0, 0, "wq")
+    ldsx = H.matrix(sx, f32, K // 128, M, "sx")
+    ldw = H.matrix(wq, u8, 0, 0, "wq")
     N2 = wq.shape[0]
     if wq.shape[1] != K or N2 % 2:
         raise ValueError("wq must be [2I, K] with K = %d and as many up rows as gate rows, got %s"
@@ -781,14 +760,12 @@ def fp8_gated_gemm(xq, sx, wq, sw, h=None, scales=None, gu=None, save=False, str
         scales = torch.empty((I // 128, _pad(max(M, 1), 4)), dtype=f32, device=xq.device)
     if gu is None and save:
         gu = torch.empty((M, N2), dtype=torch.bfloat16, device=xq.device)
-    ldh = _matrix(h, u8, M, I, "h")
-    lds = _matrix(scales, f32, I // 128, M, "scales")
+    ldh = H.matrix(h, u8, M, I, "h")
+    lds = H.matrix(scales, f32, I // 128, M, "scales")
     ldgu = pgu = 0
     if gu is not None:
-        ldgu, pgu = _matrix(gu, torch.bfloat16, M, N2, "gu"), gu.data_ptr()
-    if not (xq.is_cuda and sx.is_cuda and wq.is_cuda and sw.is_cuda and h.is_cuda and scales.is_cuda
-            and (gu is None or gu.is_cuda)):
-        _on_gpu((xq, "xq"), (sx, "sx"), (wq, "wq"), (sw, "sw"), (h, "h"), (scales, "scales"), (gu, "gu"))
+        ldgu, pgu = H.matrix(gu, torch.bfloat16, M, N2, "gu"), gu.data_ptr()
+    H.on_gpu(xq, "xq", sx, "sx", wq, "wq", sw, "sw", h, "h", scales, "scales", gu, "gu")
     rc = lib().fp8_gated_gemm(xq.data_ptr(), sx.data_ptr(), ldx, ldsx, wq.data_ptr(), sw.data_ptr(), ldw, M, I, K,
                               h.data_ptr(), ldh, scales.data_ptr(), lds, pgu, ldgu, 1 if pow2 else 0, _stream(None))
     if rc:
@@ -806,10 +783,10 @@ def fp8_gated_bwd(gu, dh, q=None, scales=None, qT=None, scalesT=None, hqT=None, 
     projection's wgrad operand)."""
     if stream is not None:
         return _under(stream, fp8_gated_bwd, gu, dh, q, scales, qT, scalesT, hqT, hscalesT, None, pow2)
-    torch = _torch()
+    torch, H = _torch(), _checks()
     u8, f32, bf16 = torch.uint8, torch.float32, torch.bfloat16
-    ldgu = _matrix(gu, bf16, 0, 0, "gu")
-    lddh = _matrix(dh, bf16, 0, 0, "dh")
+    ldgu = H.matrix(gu, bf16, 0, 0, "gu")
+    lddh = H.matrix(dh, bf16, 0, 0, "dh")
     M, I = dh.shape
     if gu.shape != (M, 2 * I):
         raise ValueError("gu must be [%d, %d], got %s" % (M, 2 * I, tuple(gu.shape)))
@@ -826,13 +803,11 @@ def fp8_gated_bwd(gu, dh, q=None, scales=None, qT=None, scalesT=None, hqT=None, 
         hqT = torch.empty((I, M), dtype=u8, device=dev)
     if hscalesT is None:
         hscalesT = torch.empty((M // 128, _pad(max(I, 1), 4)), dtype=f32, device=dev)
-    ldq, lds = _matrix(q, u8, M, 2 * I, "q"), _matrix(scales, f32, 2 * I // 128, M, "scales")
-    ldqT, ldsT = _matrix(qT, u8, 2 * I, M, "qT"), _matrix(scalesT, f32, M // 128, 2 * I, "scalesT")
-    ldhT, ldhs = _matrix(hqT, u8, I, M, "hqT"), _matrix(hscalesT, f32, M // 128, I, "hscalesT")
-    if not (gu.is_cuda and dh.is_cuda and q.is_cuda and scales.is_cuda and qT.is_cuda and scalesT.is_cuda
-            and hqT.is_cuda and hscalesT.is_cuda):
-        _on_gpu((gu, "gu"), (dh, "dh"), (q, "q"), (scales, "scales"), (qT, "qT"), (scalesT, "scalesT"), (hqT, "hqT"),
-                (hscalesT, "hscalesT"))
+    ldq, lds = H.matrix(q, u8, M, 2 * I, "q"), H.matrix(scales, f32, 2 * I // 128, M, "scales")
+    ldqT, ldsT = H.matrix(qT, u8, 2 * I, M, "qT"), H.matrix(scalesT, f32, M // 128, 2 * I, "scalesT")
+    ldhT, ldhs = H.matrix(hqT, u8, I, M, "hqT"), H.matrix(hscalesT, f32, M // 128, I, "hscalesT")
+    H.on_gpu(gu, "gu", dh, "dh", q, "q", scales, "scales", qT, "qT", scalesT, "scalesT", hqT, "hqT", hscalesT,
+             "hscalesT")
     rc = lib().fp8_gated_bwd(gu.data_ptr(), ldgu, dh.data_ptr(), lddh, M, I, q.data_ptr(), ldq, scales.data_ptr(), lds,
                              qT.data_ptr(), ldqT, scalesT.data_ptr(), ldsT, hqT.data_ptr(), ldhT, hscalesT.data_ptr(),
                              ldhs, 1 if pow2 else 0, _stream(None))
@@ -851,7 +826,7 @@ def grad_clip(grads, max_norm, eps=1e-6, out=None, norm=None, stream=None):
     / (norm + eps)); nothing is copied to the host."""
     if stream is not None:
         return _under(stream, grad_clip, grads, max_norm, eps, out, norm)
-    torch = _torch()
+    torch, H = _torch(), _checks()
     grads = list(grads)
     outs = grads if out is None else list(out)
     n = len(grads)
@@ -859,12 +834,11 @@ def grad_clip(grads, max_norm, eps=1e-6, out=None, norm=None, stream=None):
         raise ValueError("out must hold one tensor per gradient")
     if not n:
         raise ValueError("grads must hold at least one tensor")
-    table = _tensor_list().describe(grads, outs)
+    table = H.describe(grads, outs)
     if norm is None:
         norm = torch.empty(2, dtype=torch.float32, device=grads[0].device)
-    _vector(norm, torch.float32, 2, "norm")
-    if norm.device != grads[0].device:
-        raise ValueError("norm must be on the gradients' device")
+    H.vector(norm, torch.float32, 2, "norm")
+    H.on_gpu(grads[0], "grads", norm, "norm")
     L = lib()
     nbytes = L.fp8fg_grad_clip_workspace(n)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=norm.device)

@@ -21,7 +21,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfp8fg.so")
 HELPER = os.path.join(HERE, "_tensors.so")
-HELPER_SOURCE = os.path.join(CSRC, "tensor_list.cpp")
+HELPER_SOURCE = os.path.join(CSRC, "tensors.cpp")
 SOURCES = ["capi.cu", "quant.cu", "gemm.cu", "gemm_mx.cu", "moe.cu", "norm.cu", "gemm_gated.cu", "gated_bwd.cu",
            "clip.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -1,0 +1,189 @@
+// CPython helper of the binding: the argument checks of its short calls, and
+// the table that fp8fg_grad_clip reads, from torch tensors.
+//
+// Looking at one property of a tensor from Python takes 0.07 to 0.15 us, a
+// check of its type, layout and extent half a microsecond with the call: for a
+// decoding step's norm that was more than the kernel, and for the gradients of
+// a whole model many times the library's own work. Here it takes a few
+// nanoseconds. This module only reads the tensors' metadata; it is compiled
+// against the installed torch.
+#define PY_SSIZE_T_CLEAN
+#include <Python.h>
+
+#include <exception>
+
+#include <torch/csrc/Dtype.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include "fp8fg.h"
+
+namespace {
+
+PyObject *refuse(const char *what)
+{
+    PyErr_SetString(PyExc_ValueError, what);
+    return nullptr;
+}
+
+// f(), with a C++ exception (a tensor without storage, for example) as ValueError
+template <typename F>
+PyObject *guarded(F f)
+{
+    try {
+        return f();
+    } catch (const std::exception &e) {
+        PyErr_SetString(PyExc_ValueError, e.what());
+        return nullptr;
+    }
+}
+
+// describe(grads, outs) -> bytes: one fp8fg_grad per tensor of the two lists
+// (of the same length; outs may be grads itself). Raises ValueError for what
+// the kernels cannot take; the device is looked at last.
+PyObject *describe_checked(PyObject *grads, PyObject *outs)
+{
+    const Py_ssize_t n = PyList_GET_SIZE(grads);
+    PyObject *table = PyBytes_FromStringAndSize(nullptr, n * (Py_ssize_t)sizeof(fp8fg_grad));
+    if (!table)
+        return nullptr;
+    fp8fg_grad *row = reinterpret_cast<fp8fg_grad *>(PyBytes_AS_STRING(table));
+    const char *bad = nullptr;
+    bool cuda = true, one_device = true;
+    c10::Device device(c10::DeviceType::CPU);
+    for (Py_ssize_t i = 0; i < n && !bad; ++i) {
+        PyObject *go = PyList_GET_ITEM(grads, i), *oo = PyList_GET_ITEM(outs, i);
+        if (!THPVariable_Check(go) || !THPVariable_Check(oo)) {
+            bad = "grads and out must hold tensors";
+            break;
+        }
+        const at::Tensor &g = THPVariable_Unpack(go), &o = THPVariable_Unpack(oo);
+        const at::ScalarType type = g.scalar_type();
+        if (type != at::kFloat && type != at::kBFloat16)
+            bad = "gradients must be float32 or bfloat16";
+        else if (o.scalar_type() != type || o.numel() != g.numel())
+            bad = "out must match the gradients' sizes and types";
+        else if (g.layout() != at::kStrided || o.layout() != at::kStrided || !g.is_contiguous() || !o.is_contiguous())
+            bad = "gradients and out must be contiguous";
+        if (bad)
+            break;
+        if (i == 0)
+            device = g.device();
+        cuda = cuda && g.is_cuda() && o.is_cuda();
+        one_device = one_device && g.device() == device && o.device() == device;
+        row[i].g = g.const_data_ptr();
+        row[i].out = o.mutable_data_ptr();
+        row[i].n = g.numel();
+        row[i].kind = type == at::kFloat ? FP8FG_OUT_F32 : FP8FG_OUT_BF16;
+        row[i].unused = 0;
+    }
+    if (!bad && !cuda)
+        bad = "grads and out must be CUDA tensors";
+    if (!bad && !one_device)
+        bad = "grads and out must be on one device";
+    if (bad) {
+        Py_DECREF(table);
+        return refuse(bad);
+    }
+    return table;
+}
+
+PyObject *describe(PyObject *, PyObject *const *args, Py_ssize_t nargs)
+{
+    if (nargs != 2 || !PyList_Check(args[0]) || !PyList_Check(args[1]) ||
+        PyList_GET_SIZE(args[0]) != PyList_GET_SIZE(args[1]))
+        return refuse("describe takes two lists of the same length");
+    return guarded([&] { return describe_checked(args[0], args[1]); });
+}
+
+// Arguments (tensor, dtype, size, ..., name) shared by matrix and vector:
+// false, with the error set, when they are not that or the dtype differs.
+bool typed_tensor(PyObject *const *args, Py_ssize_t nargs, Py_ssize_t want)
+{
+    if (nargs != want || !THPDtype_Check(args[1]) || !PyUnicode_Check(args[want - 1])) {
+        refuse("bad call of the argument check");
+        return false;
+    }
+    if (!THPVariable_Check(args[0])) {
+        PyErr_Format(PyExc_ValueError, "%U must be a tensor", args[want - 1]);
+        return false;
+    }
+    const at::Tensor &t = THPVariable_Unpack(args[0]);
+    if (t.scalar_type() != reinterpret_cast<THPDtype *>(args[1])->scalar_type) {
+        PyErr_Format(PyExc_ValueError, "%U must be %S", args[want - 1], args[1]);
+        return false;
+    }
+    return true;
+}
+
+// matrix(t, dtype, rows, cols, name) -> row pitch of a 2-D row-major tensor of
+// the dtype that covers [rows, cols]
+PyObject *matrix(PyObject *, PyObject *const *args, Py_ssize_t nargs)
+{
+    return guarded([&]() -> PyObject * {
+        if (!typed_tensor(args, nargs, 5))
+            return nullptr;
+        const at::Tensor &t = THPVariable_Unpack(args[0]);
+        const long long rows = PyLong_AsLongLong(args[2]), cols = PyLong_AsLongLong(args[3]);
+        if (PyErr_Occurred())
+            return nullptr;
+        if (t.layout() != at::kStrided || t.dim() != 2 || t.stride(1) != 1)
+            return PyErr_Format(PyExc_ValueError, "%U must be a 2-D row-major tensor (unit inner stride)", args[4]);
+        if (t.size(0) < rows || t.size(1) < cols)
+            return PyErr_Format(PyExc_ValueError, "%U must cover [%lld, %lld], got (%lld, %lld)", args[4], rows, cols,
+                                (long long)t.size(0), (long long)t.size(1));
+        return PyLong_FromLongLong(t.stride(0));
+    });
+}
+
+// vector(t, dtype, n, name): a contiguous vector of at least n entries
+PyObject *vector(PyObject *, PyObject *const *args, Py_ssize_t nargs)
+{
+    return guarded([&]() -> PyObject * {
+        if (!typed_tensor(args, nargs, 4))
+            return nullptr;
+        const at::Tensor &t = THPVariable_Unpack(args[0]);
+        const long long n = PyLong_AsLongLong(args[2]);
+        if (PyErr_Occurred())
+            return nullptr;
+        if (t.layout() != at::kStrided || t.dim() != 1 || t.numel() < n || !t.is_contiguous())
+            return PyErr_Format(PyExc_ValueError, "%U must be a contiguous vector of at least %lld entries", args[3], n);
+        Py_RETURN_NONE;
+    });
+}
+
+// on_gpu(t, name, t, name, ...): every tensor (None is skipped) is a CUDA
+// tensor, all on one device
+PyObject *on_gpu(PyObject *, PyObject *const *args, Py_ssize_t nargs)
+{
+    return guarded([&]() -> PyObject * {
+        c10::Device device(c10::DeviceType::CPU);
+        for (Py_ssize_t i = 0; i + 1 < nargs; i += 2) {
+            if (args[i] == Py_None)
+                continue;
+            if (!THPVariable_Check(args[i]) || !THPVariable_Unpack(args[i]).is_cuda())
+                return PyErr_Format(PyExc_ValueError, "%U must be a CUDA tensor", args[i + 1]);
+            const c10::Device d = THPVariable_Unpack(args[i]).device();
+            if (device.is_cpu())
+                device = d;
+            if (d != device)
+                return PyErr_Format(PyExc_ValueError, "%U must be on the other tensors' device", args[i + 1]);
+        }
+        Py_RETURN_NONE;
+    });
+}
+
+template <typename F>
+PyCFunction fast(F f) { return reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(f)); }
+
+PyMethodDef methods[] = {
+    {"describe", fast(describe), METH_FASTCALL, "describe(grads, outs) -> bytes of fp8fg_grad rows"},
+    {"matrix", fast(matrix), METH_FASTCALL, "matrix(t, dtype, rows, cols, name) -> row pitch"},
+    {"vector", fast(vector), METH_FASTCALL, "vector(t, dtype, n, name)"},
+    {"on_gpu", fast(on_gpu), METH_FASTCALL, "on_gpu(t, name, t, name, ...)"},
+    {nullptr, nullptr, 0, nullptr}};
+
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__tensors(void) { return PyModule_Create(&module); }

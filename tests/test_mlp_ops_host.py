@@ -18,7 +18,7 @@ A, ODD = 0x10000, 0x10008          # never dereferenced
 BF16, U8, F32 = torch.bfloat16, torch.uint8, torch.float32
 
 
-@pytest.fixture(scope="module")
+@pytest.fixture(scope="module", autouse=True)
 def L():
     libbuild.build()
     return fg.lib()
@@ -160,6 +160,10 @@ def test_binding_norm():
     expect("scales must cover", fg.fp8_rmsnorm, x, w, scales=z((2, 3), F32))
     expect("rstd", fg.fp8_rmsnorm, x, w, rstd=z((3,), F32))
     expect("rstd", fg.fp8_rmsnorm, x, w, rstd=z((8,), F32)[::2])
+    expect("x must be a tensor", fg.fp8_rmsnorm, [1.0], w)
+    expect("rstd must be a tensor", fg.fp8_rmsnorm, x, w, rstd=3)
+    expect("row-major", fg.fp8_rmsnorm, x.to_sparse(), w)
+    expect("row-major", fg.fp8_rmsnorm, z((4, 2, 128), BF16), w)
 
 
 def test_binding_norm_transposed_and_backward():
@@ -251,9 +255,26 @@ def test_code_check_finds_wrong_codes_and_scales():
         R.check_codes(codes, off, ref, 0.0)
 
 
+def test_checks_of_the_helper():
+    from fp8_fine_grained_gb300 import _tensors as H
+    m = z((6, 10), BF16)[:, 2:8]
+    assert H.matrix(m, BF16, 6, 6, "m") == 10
+    assert H.matrix(z((0, 5), U8), U8, 0, 5, "m") == 5
+    assert H.vector(z((4,), F32), F32, 3, "v") is None
+    assert H.on_gpu(None, "a", None, "b") is None
+    expect("m must cover", H.matrix, m, BF16, 7, 6, "m")
+    expect("m must be torch.uint8", H.matrix, m, U8, 1, 1, "m")
+    expect("v must be a contiguous vector of at least 5", H.vector, z((4,), F32), F32, 5, "v")
+    expect("b must be a CUDA tensor", H.on_gpu, None, "a", m, "b")
+    for args in ((), (m, BF16, 1, 1), (m, 3, 1, 1, "m"), (m, BF16, 1, 1, 7)):
+        expect("bad call", H.matrix, *args)
+    with pytest.raises(TypeError):
+        H.matrix(m, BF16, 1.5, 1, "m")
+
+
 def test_tensor_table():
-    """The rows that the helper writes, read back as the C structure, and its
-    refusals (the device is looked at last)."""
+    """The refusals of the helper that writes the clipping's table (the device
+    is looked at last)."""
     from fp8_fine_grained_gb300 import _tensors
     flat = torch.arange(20, dtype=F32)
     with pytest.raises(ValueError, match="CUDA"):
