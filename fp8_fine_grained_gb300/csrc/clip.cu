@@ -326,7 +326,8 @@ int launch_scale(const fp8fg_grad *t, int take, const double *partial, int n_par
 {
     Table<N> tab;
     fill(tab, t, take, SCALE_UNROLL);
-    return launch_pss(scale_kernel<N>, dim3(grid_of(tab.first[take])), THREADS, 0, s, tab, partial, n_partial, max_norm, eps, norm);
+    return launch_pss(scale_kernel<N>, dim3(grid_of(tab.first[take])), THREADS, 0, s, tab, partial, n_partial, max_norm,
+                      eps, norm);
 }
 
 }  // namespace

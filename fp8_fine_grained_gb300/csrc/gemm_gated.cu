@@ -192,6 +192,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr int NS = SH::STAGES, NB = SH::BUFS, TOK = SH::TOK;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
+    // the swizzled stages assume the alignment requested above (the same for
+    // every CTA): refuse to run if it is missing
+    if (sbase & 1023u) {
+        if (threadIdx.x == 0)
+            atomicCAS(p.status, 0, FP8FG_EUNSUPPORTED);
+        return;
+    }
     const uint32_t full_bar = sbase + SH::full_off, empty_bar = sbase + SH::empty_off;
     const uint32_t tempty_bar = sbase + SH::tempty_off, tfull_bar = sbase + SH::tfull_off;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + SH::abort_off);

@@ -129,8 +129,8 @@ __device__ __forceinline__ float block_sum(float v, float *part, int nwarps)
 }
 
 // Dynamic shared memory: the ring, `slots` slots of `tensors` rows of D bf16
-// values each; one "row landed" barrier per slot; gamma where it is staged. Rows are the
-// CTA's own: blockIdx, blockIdx + grid, ...
+// values each; one "row landed" barrier per slot; gamma where it is staged.
+// Rows are the CTA's own: blockIdx, blockIdx + grid, ...
 constexpr int MAX_SLOTS = 8;
 constexpr uint32_t BAR_BYTES = 8 * MAX_SLOTS;
 
