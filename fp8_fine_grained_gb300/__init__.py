@@ -609,15 +609,6 @@ def fp8_moe_combine(y, dest, w, out_dtype=None, out=None, stream=None):
 # come from that stream's memory, so that no work still queued on the current
 # stream can be using it.
 
-def _gamma_kind(H, gamma, D):
-    """OUT_BF16 or OUT_F32 of a norm's weight of D entries."""
-    kind = _out_code(gamma.dtype)
-    H.vector(gamma, gamma.dtype, D, "gamma")
-    if gamma.shape[0] != D:
-        raise ValueError("gamma must hold %d entries, got %d" % (D, gamma.shape[0]))
-    return kind
-
-
 def _under(stream, fn, *args, **kw):
     with _torch().cuda.stream(stream):
         return fn(*args, **kw)
@@ -638,7 +629,7 @@ def fp8_rmsnorm(x, gamma, eps=1e-6, residual=None, h=None, q=None, scales=None, 
     bf16, f32, u8 = torch.bfloat16, torch.float32, torch.uint8
     ldx = H.matrix(x, bf16, 0, 0, "x")
     T, D = x.shape
-    kind = _gamma_kind(H, gamma, D)
+    kind = H.norm_weight(gamma, D)
     ldr = ldh = pr = ph = 0
     if residual is not None:
         ldr = H.matrix(residual, bf16, T, D, "residual")
@@ -677,7 +668,7 @@ def fp8_rmsnorm_t(h, rstd, gamma, qT=None, scalesT=None, stream=None, pow2=False
     f32, u8 = torch.float32, torch.uint8
     ldh = H.matrix(h, torch.bfloat16, 0, 0, "h")
     T, D = h.shape
-    kind = _gamma_kind(H, gamma, D)
+    kind = H.norm_weight(gamma, D)
     H.vector(rstd, f32, T, "rstd")
     if qT is None:
         qT = torch.empty((D, T), dtype=u8, device=h.device)
@@ -707,7 +698,7 @@ def fp8_rmsnorm_bwd(dy, h, rstd, gamma, dres=None, dx=None, dgamma=None, stream=
     T, D = dy.shape
     ldh = H.matrix(h, bf16, T, D, "h")
     H.vector(rstd, f32, T, "rstd")
-    kind = _gamma_kind(H, gamma, D)
+    kind = H.norm_weight(gamma, D)
     lddres = pdres = 0
     if dres is not None:
         lddres, pdres = H.matrix(dres, bf16, T, D, "dres"), dres.data_ptr()

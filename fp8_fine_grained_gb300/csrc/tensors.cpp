@@ -151,6 +151,27 @@ PyObject *vector(PyObject *, PyObject *const *args, Py_ssize_t nargs)
     });
 }
 
+// norm_weight(gamma, D) -> FP8FG_OUT_F32 or FP8FG_OUT_BF16: a norm's weight, a
+// contiguous vector of exactly D entries
+PyObject *norm_weight(PyObject *, PyObject *const *args, Py_ssize_t nargs)
+{
+    return guarded([&]() -> PyObject * {
+        if (nargs != 2)
+            return refuse("bad call of the argument check");
+        if (!THPVariable_Check(args[0]))
+            return refuse("gamma must be a tensor");
+        const at::Tensor &t = THPVariable_Unpack(args[0]);
+        const long long n = PyLong_AsLongLong(args[1]);
+        if (PyErr_Occurred())
+            return nullptr;
+        if (t.scalar_type() != at::kFloat && t.scalar_type() != at::kBFloat16)
+            return refuse("gamma must be float32 or bfloat16");
+        if (t.layout() != at::kStrided || t.dim() != 1 || t.numel() != n || !t.is_contiguous())
+            return PyErr_Format(PyExc_ValueError, "gamma must be a contiguous vector of %lld entries", n);
+        return PyLong_FromLong(t.scalar_type() == at::kFloat ? FP8FG_OUT_F32 : FP8FG_OUT_BF16);
+    });
+}
+
 // on_gpu(t, name, t, name, ...): every tensor (None is skipped) is a CUDA
 // tensor, all on one device
 PyObject *on_gpu(PyObject *, PyObject *const *args, Py_ssize_t nargs)
@@ -179,6 +200,7 @@ PyMethodDef methods[] = {
     {"describe", fast(describe), METH_FASTCALL, "describe(grads, outs) -> bytes of fp8fg_grad rows"},
     {"matrix", fast(matrix), METH_FASTCALL, "matrix(t, dtype, rows, cols, name) -> row pitch"},
     {"vector", fast(vector), METH_FASTCALL, "vector(t, dtype, n, name)"},
+    {"norm_weight", fast(norm_weight), METH_FASTCALL, "norm_weight(gamma, D) -> output kind of its type"},
     {"on_gpu", fast(on_gpu), METH_FASTCALL, "on_gpu(t, name, t, name, ...)"},
     {nullptr, nullptr, 0, nullptr}};
 

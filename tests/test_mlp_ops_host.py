@@ -151,7 +151,7 @@ def test_binding_norm():
     expect("row-major", fg.fp8_rmsnorm, z((256, 4), BF16).t(), w)
     expect("gamma", fg.fp8_rmsnorm, x, w[:128])
     expect("gamma", fg.fp8_rmsnorm, x, z((512,), BF16)[::2])
-    expect("dtype", fg.fp8_rmsnorm, x, w.double())
+    expect("float32 or bfloat16", fg.fp8_rmsnorm, x, w.double())
     expect("residual", fg.fp8_rmsnorm, x, w, residual=x[:3])
     expect("residual", fg.fp8_rmsnorm, x, w, residual=x.float())
     expect("h must cover", fg.fp8_rmsnorm, x, w, residual=x, h=z((3, 256), BF16))
@@ -262,6 +262,10 @@ def test_checks_of_the_helper():
     assert H.matrix(z((0, 5), U8), U8, 0, 5, "m") == 5
     assert H.vector(z((4,), F32), F32, 3, "v") is None
     assert H.on_gpu(None, "a", None, "b") is None
+    assert H.norm_weight(z((5,), F32), 5) == fg.OUT_F32 and H.norm_weight(z((5,), BF16), 5) == fg.OUT_BF16
+    expect("gamma must be a contiguous vector of 4", H.norm_weight, z((5,), F32), 4)
+    expect("gamma must be a contiguous vector of 5", H.norm_weight, z((10,), F32)[::2], 5)
+    expect("gamma must be a tensor", H.norm_weight, [1.0], 1)
     expect("m must cover", H.matrix, m, BF16, 7, 6, "m")
     expect("m must be torch.uint8", H.matrix, m, U8, 1, 1, "m")
     expect("v must be a contiguous vector of at least 5", H.vector, z((4,), F32), F32, 5, "v")
