@@ -38,14 +38,12 @@ PyObject *guarded(F f)
 }
 
 // describe(grads, outs) -> bytes: one fp8fg_grad per tensor of the two lists
-// (of the same length; outs may be grads itself). Raises ValueError for what
-// the kernels cannot take; the device is looked at last.
-PyObject *describe_checked(PyObject *grads, PyObject *outs)
+// (of the same length; outs may be grads itself), written into `table`, which
+// is returned. Raises ValueError for what the kernels cannot take; the device
+// is looked at last.
+PyObject *describe_into(PyObject *table, PyObject *grads, PyObject *outs)
 {
     const Py_ssize_t n = PyList_GET_SIZE(grads);
-    PyObject *table = PyBytes_FromStringAndSize(nullptr, n * (Py_ssize_t)sizeof(fp8fg_grad));
-    if (!table)
-        return nullptr;
     fp8fg_grad *row = reinterpret_cast<fp8fg_grad *>(PyBytes_AS_STRING(table));
     const char *bad = nullptr;
     bool cuda = true, one_device = true;
@@ -80,11 +78,7 @@ PyObject *describe_checked(PyObject *grads, PyObject *outs)
         bad = "grads and out must be CUDA tensors";
     if (!bad && !one_device)
         bad = "grads and out must be on one device";
-    if (bad) {
-        Py_DECREF(table);
-        return refuse(bad);
-    }
-    return table;
+    return bad ? refuse(bad) : table;
 }
 
 PyObject *describe(PyObject *, PyObject *const *args, Py_ssize_t nargs)
@@ -92,7 +86,14 @@ PyObject *describe(PyObject *, PyObject *const *args, Py_ssize_t nargs)
     if (nargs != 2 || !PyList_Check(args[0]) || !PyList_Check(args[1]) ||
         PyList_GET_SIZE(args[0]) != PyList_GET_SIZE(args[1]))
         return refuse("describe takes two lists of the same length");
-    return guarded([&] { return describe_checked(args[0], args[1]); });
+    PyObject *table =
+        PyBytes_FromStringAndSize(nullptr, PyList_GET_SIZE(args[0]) * (Py_ssize_t)sizeof(fp8fg_grad));
+    if (!table)
+        return nullptr;
+    PyObject *rows = guarded([&] { return describe_into(table, args[0], args[1]); });
+    if (!rows)
+        Py_DECREF(table);
+    return rows;
 }
 
 // Arguments (tensor, dtype, size, ..., name) shared by matrix and vector:
@@ -146,7 +147,8 @@ PyObject *vector(PyObject *, PyObject *const *args, Py_ssize_t nargs)
         if (PyErr_Occurred())
             return nullptr;
         if (t.layout() != at::kStrided || t.dim() != 1 || t.numel() < n || !t.is_contiguous())
-            return PyErr_Format(PyExc_ValueError, "%U must be a contiguous vector of at least %lld entries", args[3], n);
+            return PyErr_Format(PyExc_ValueError, "%U must be a contiguous vector of at least %lld entries", args[3],
+                                n);
         Py_RETURN_NONE;
     });
 }
