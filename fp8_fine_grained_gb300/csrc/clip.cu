@@ -220,7 +220,6 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     scale_kernel(const __grid_constant__ Table<N> tab, const double *__restrict__ partial, int n_partial,
                  float max_norm, float eps, float *norm_out)
 {
-    griddep_launch_dependents();
     griddep_wait();
     __shared__ double part[THREADS / 32];
     double total = 0.0;
@@ -269,6 +268,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
         if ((int)threadIdx.x < q.head)
             store_one(q.out, threadIdx.x, q.bf16, load_one(q.g, threadIdx.x, q.bf16) * coef);
     }
+    griddep_launch_dependents();  // (not on entry: the sums of a following call would start among these CTAs)
 }
 
 // CTAs of a launch: all resident at once.
@@ -380,17 +380,17 @@ extern "C" int fp8fg_grad_clip(const fp8fg_grad *grads, int64_t count, float max
             int rc;
             if (pass == 0) {
                 int used = 0;
-                rc = take <= 64 ? launch_sumsq<64>(grads + at, take, partial + n_partial, &used, s)
-                                : (take <= 256 ? launch_sumsq<256>(grads + at, take, partial + n_partial, &used, s)
-                                               : launch_sumsq<MAX_TENSORS>(grads + at, take, partial + n_partial, &used, s));
+                auto sums = take <= 64    ? launch_sumsq<64>
+                            : take <= 256 ? launch_sumsq<256>
+                                          : launch_sumsq<MAX_TENSORS>;
+                rc = sums(grads + at, take, partial + n_partial, &used, s);
                 n_partial += used;
             } else {
                 float *out = at == 0 ? norm : nullptr;
-                rc = take <= 64 ? launch_scale<64>(grads + at, take, partial, n_partial, max_norm, eps, out, s)
-                                : (take <= 256
-                                       ? launch_scale<256>(grads + at, take, partial, n_partial, max_norm, eps, out, s)
-                                       : launch_scale<MAX_TENSORS>(grads + at, take, partial, n_partial, max_norm, eps,
-                                                                   out, s));
+                auto scaled = take <= 64    ? launch_scale<64>
+                              : take <= 256 ? launch_scale<256>
+                                            : launch_scale<MAX_TENSORS>;
+                rc = scaled(grads + at, take, partial, n_partial, max_norm, eps, out, s);
             }
             if (rc != FP8FG_OK)
                 return rc;

@@ -24,6 +24,8 @@
 // the last store, so each tensor crosses the memory once.
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "group_rule.cuh"
 #include "host_common.h"
 #include "ptx.cuh"
@@ -131,8 +133,17 @@ __device__ __forceinline__ float block_sum(float v, float *part, int nwarps)
 // Dynamic shared memory: the ring, `slots` slots of `tensors` rows of D bf16
 // values each; one "row landed" barrier per slot; gamma where it is staged.
 // Rows are the CTA's own: blockIdx, blockIdx + grid, ...
-constexpr int MAX_SLOTS = 8;
-constexpr uint32_t BAR_BYTES = 8 * MAX_SLOTS;
+//
+// The rows are dealt out evenly, so every SM has to hold the same number of
+// CTAs. A kernel that let the next one start on entry would see that one's
+// CTAs placed unevenly, on whichever SMs drain first, so a CTA lets the
+// next kernel start after its last row (on entry when it has one row only:
+// there the next kernel's set-up hides behind this one), and the shared memory
+// asked for leaves no room for a further CTA on the SM. 8192 rows of 7168
+// after another kernel: 36.5 us (without a residual), with an early start and
+// without the padding 42.4; backward of 28672 rows of 2048: 59.3, early 92.
+constexpr int MAX_SLOTS = 3;
+constexpr uint32_t BAR_BYTES = (8 * MAX_SLOTS + 15) / 16 * 16;  // (gamma follows)
 
 // Where gamma is staged in shared memory: in the backward pass, which reads it
 // twice per row, and in the forward pass without a residual (8192 x 7168: 39 us,
@@ -193,7 +204,7 @@ struct NormFwd {
     int64_t T, ldx, ldr, ldh, ldq, ld_s;
     int D;
     float eps;
-    bool gamma_f32;
+    bool gamma_f32, one_row;  // one_row: per CTA
     int slots;
     int *status;
     uint64_t wait_limit_ns;
@@ -231,7 +242,8 @@ __global__ void __launch_bounds__(max_threads(W), min_ctas(W, false)) rmsnorm_fw
         pending |= 1u << slot;
         parity = (parity & ~(1u << slot)) | (par << slot);
     };
-    griddep_launch_dependents();
+    if (p.one_row)
+        griddep_launch_dependents();
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.slots; ++s)
             mbar_init(ring.bars + 8 * s, 1);
@@ -323,6 +335,8 @@ __global__ void __launch_bounds__(max_threads(W), min_ctas(W, false)) rmsnorm_fw
             }
         }
     }
+    if (!p.one_row)
+        griddep_launch_dependents();
     if (threadIdx.x == 0 && *wc.abort_flag)
         drain(ring, pending, parity, p.wait_limit_ns);
 }
@@ -411,7 +425,7 @@ struct NormBwd {
     float *part;  // [gridDim.x][D]
     int64_t T, lddy, ldh, lddres, lddx;
     int D;
-    bool gamma_f32;
+    bool gamma_f32, one_row;  // one_row: per CTA
     int slots;
     int *status;
     uint64_t wait_limit_ns;
@@ -454,7 +468,8 @@ __global__ void __launch_bounds__(max_threads(W), min_ctas(W, true)) rmsnorm_bwd
         pending |= 1u << slot;
         parity = (parity & ~(1u << slot)) | (par << slot);
     };
-    griddep_launch_dependents();
+    if (p.one_row)
+        griddep_launch_dependents();
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.slots; ++s)
             mbar_init(ring.bars + 8 * s, 1);
@@ -545,6 +560,8 @@ __global__ void __launch_bounds__(max_threads(W), min_ctas(W, true)) rmsnorm_bwd
             o[1] = make_float4(dg[i][2].x, dg[i][2].y, dg[i][3].x, dg[i][3].y);
         }
     }
+    if (!p.one_row)
+        griddep_launch_dependents();
     if (threadIdx.x == 0 && *wc.abort_flag)
         drain(ring, pending, parity, p.wait_limit_ns);
 }
@@ -558,7 +575,6 @@ constexpr int DG_THREADS = 8 * DG_SLICES;
 __global__ void __launch_bounds__(DG_THREADS) norm_dgamma_kernel(const float4 *__restrict__ part, int rows, int D,
                                                                  float *__restrict__ dgamma)
 {
-    griddep_launch_dependents();
     griddep_wait();
     __shared__ float4 s[DG_SLICES][8];
     __shared__ float s8[8][32];
@@ -589,6 +605,7 @@ __global__ void __launch_bounds__(DG_THREADS) norm_dgamma_kernel(const float4 *_
             a += s8[i][c];
         dgamma[blockIdx.x * 32 + c] = a;
     }
+    griddep_launch_dependents();
 }
 
 // Width and threads of a row of D columns: up to four chunks per thread,
@@ -611,30 +628,33 @@ struct RingShape {
     size_t smem;
 };
 
-// Forward: as many CTAs as the registers allow with two rows each in flight
-// (one row's reduction runs under another's loads and stores), or two CTAs with
-// three rows (8191 x 7168 with a residual: 65 us; three with two 68).
-// Backward: four rows each in flight rather than more CTAs, each of which adds
-// a row to dgamma's partial sums (16384 x 2048 with dres: 4 CTAs of 4 rows
-// 46 us, 8 of 2 60 us), down to two CTAs of two rows.
+// Two slots: a row's reduction runs under the next row's copies. Forward: as
+// many CTAs as fit (more slots for fewer CTAs were slower at every width from
+// 256 to 18432). Backward: each CTA adds a row to dgamma's partial sums, so the
+// fewest CTAs with 96 KB in flight (28672 x 2048 with dres: 4 CTAs 75 us, 6
+// 78; 2 slots or 4 the same), but two, since one CTA leaves the memory idle at
+// its barriers; where two do not fit, one with three slots (8192 columns with
+// dres: 76 us, with two slots 79). The widest rows read gamma through L1, whose
+// space a third slot or padding would take (12288 columns with dres: 88 us,
+// with three slots 104).
 RingShape ring_shape(int64_t D, int tensors, bool gamma_f32, bool bwd)
 {
     const RowShape rs = row_shape(D);
     const int64_t gamma_bytes = stages_gamma(rs.width, bwd, tensors) ? (gamma_f32 ? 4 * D : 2 * D) : 0;
-    constexpr int64_t SM_BYTES = 226 * 1024;                      // of an SM
-    const int64_t beside = gamma_bytes + BAR_BYTES + 1024 + 512;  // of a CTA beside the ring, 1 KB of it the system's
-    const int64_t slot = 2 * D * tensors;
-    auto slots_of = [&](int per_sm) {
-        const int64_t n = (SM_BYTES / per_sm - beside) / slot;
-        return (int)(n > MAX_SLOTS ? MAX_SLOTS : n);
-    };
+    constexpr int64_t SM_BYTES = 226 * 1024;  // of an SM
+    constexpr int64_t OWN = 1024 + 512;       // of a CTA beside its dynamic part, 1 KB of it the system's
+    constexpr int64_t IN_FLIGHT = 96 * 1024;
+    const int64_t slot = 2 * D * tensors, fixed = gamma_bytes + BAR_BYTES;
     int per_sm = max_threads(rs.width) * min_ctas(rs.width, bwd) / rs.threads;
-    while (per_sm > 2 && slots_of(per_sm) < (bwd ? 4 : (per_sm == 3 ? 3 : 2)))
+    if (bwd) {
+        const int64_t want = std::max<int64_t>(2, (IN_FLIGHT + 2 * slot - 1) / (2 * slot));
+        per_sm = (int)std::min<int64_t>(per_sm, want);
+    }
+    while (per_sm > 1 && (2 * slot + fixed + OWN) * per_sm > SM_BYTES)
         --per_sm;
-    if (slots_of(per_sm) < 2)
-        per_sm = 1;
-    const int slots = slots_of(per_sm);
-    return {per_sm, slots, (size_t)(slots * slot + BAR_BYTES + gamma_bytes)};
+    const int slots = per_sm == 1 && rs.width != WIDE && 3 * slot + fixed + OWN <= SM_BYTES ? 3 : 2;
+    const int64_t smem = slots * slot + fixed, room = (SM_BYTES / per_sm - OWN) / 128 * 128;
+    return {per_sm, slots, (size_t)(rs.width != WIDE && smem < room ? room : smem)};
 }
 
 int ring_grid(int64_t T, const RingShape &r)
@@ -713,6 +733,7 @@ extern "C" int fp8_rmsnorm(const void *x, int64_t ldx, const void *residual, int
     const RingShape ring = ring_shape(D, residual ? 2 : 1, p.gamma_f32, false);
     const int grid = ring_grid(T, ring);
     p.slots = ring.slots;
+    p.one_row = T <= grid;
     p.status = status_word_ptr();
     p.wait_limit_ns = wait_limit_ns();
     if (!p.status)
@@ -748,9 +769,8 @@ extern "C" int fp8_rmsnorm_t(const void *h, int64_t ldh, const float *rstd, cons
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const uint16_t *hp = static_cast<const uint16_t *>(h);
     const bool f32 = gamma_kind == FP8FG_OUT_F32;
-    return pow2 ? launch_pss(rmsnorm_t_kernel<true>, grid, 256, 0, s, hp, ldh, rstd, gamma, f32, D, qT, ldqT, scalesT, ld_sT)
-                : launch_pss(rmsnorm_t_kernel<false>, grid, 256, 0, s, hp, ldh, rstd, gamma, f32, D, qT, ldqT, scalesT,
-                             ld_sT);
+    auto k = pow2 ? rmsnorm_t_kernel<true> : rmsnorm_t_kernel<false>;
+    return launch_pss(k, grid, 256, 0, s, hp, ldh, rstd, gamma, f32, D, qT, ldqT, scalesT, ld_sT);
 }
 
 extern "C" int64_t fp8_rmsnorm_bwd_workspace(int64_t T, int64_t D)
@@ -812,6 +832,7 @@ extern "C" int fp8_rmsnorm_bwd(const void *dy, int64_t lddy, const void *h, int6
     p.gamma_f32 = gamma_kind == FP8FG_OUT_F32;
     const RowShape rs = row_shape(D);
     p.slots = ring.slots;
+    p.one_row = T <= grid;
     p.status = status_word_ptr();
     p.wait_limit_ns = wait_limit_ns();
     if (!p.status)
