@@ -130,6 +130,34 @@ __device__ __forceinline__ float block_sum(float v, float *part, int nwarps)
     return v;
 }
 
+// A half-warp's CPT groups (chunk i of its 16 threads is group i) are reduced
+// together: each exchange also halves the groups that a thread still holds, 5
+// shuffles for four groups in place of 16. Group i's maximum ends in the
+// LANES threads from i * LANES on, which share the division sequence of
+// its scales.
+template <int CPT> constexpr int LANES = CPT == 1 ? 16 : (CPT == 2 ? 8 : 4);
+
+template <int CPT>
+__device__ __forceinline__ float group_max(const float (&m)[CPT])
+{
+    const int lane = threadIdx.x;
+    float v = m[0];
+    if constexpr (CPT > 2) {
+        const bool hi = lane & 8, odd = lane & 4;
+        const float m3 = CPT > 3 ? m[CPT - 1] : 0.0f;
+        const float a = fmaxf(hi ? m[2] : m[0], __shfl_xor_sync(0xffffffffu, hi ? m[0] : m[2], 8));
+        const float b = fmaxf(hi ? m3 : m[1], __shfl_xor_sync(0xffffffffu, hi ? m[1] : m3, 8));
+        v = fmaxf(odd ? b : a, __shfl_xor_sync(0xffffffffu, odd ? a : b, 4));
+    } else if constexpr (CPT == 2) {
+        const bool hi = lane & 8;
+        v = fmaxf(hi ? m[1] : m[0], __shfl_xor_sync(0xffffffffu, hi ? m[0] : m[1], 8));
+    }
+#pragma unroll
+    for (int o = LANES<CPT> / 2; o >= 1; o >>= 1)
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
 // Dynamic shared memory: the ring, `slots` slots of `tensors` rows of D bf16
 // values each; one "row landed" barrier per slot; gamma where it is staged.
 // Rows are the CTA's own: blockIdx, blockIdx + grid, ...
@@ -203,7 +231,7 @@ struct NormFwd {
     float *scales, *rstd;
     int64_t T, ldx, ldr, ldh, ldq, ld_s;
     int D;
-    float eps;
+    float eps, inv_d;
     bool gamma_f32, one_row;  // one_row: per CTA
     int slots;
     int *status;
@@ -289,41 +317,36 @@ __global__ void __launch_bounds__(max_threads(W), min_ctas(W, false)) rmsnorm_fw
             if (ahead < p.T && !*wc.abort_flag)
                 fetch(ahead, ring.slot, ring.phase ^ 1);
         }
-        const float rstd = inv_sqrt(ss / (float)p.D + p.eps);
+        const float rstd = inv_sqrt(fmaf(ss, p.inv_d, p.eps));
         if (threadIdx.x == 0)
             p.rstd[t] = rstd;
-        // the groups' maxima, then one division sequence for a half-warp's CPT
-        // groups: lane i of it takes the group of chunk i
         const float2 rstd2 = splat(rstd);
         float2 y[CPT][4];
-        float mine = 0.0f;
+        float amax[CPT];
 #pragma unroll
         for (int i = 0; i < CPT; ++i) {
             const int c = threadIdx.x + i * blockDim.x;
             float2 g[4];
             unpack8(v[i], y[i]);
             load_gamma(gamma, p.gamma_f32, c < nchunk ? c : 0, g);
-            float amax = 0.0f;
+            amax[i] = 0.0f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 y[i][e] = __fmul2_rn(__fmul2_rn(y[i][e], rstd2), g[e]);
-                amax = fmaxf(amax, fmaxf(fabsf(y[i][e].x), fabsf(y[i][e].y)));
+                amax[i] = fmaxf(amax[i], fmaxf(fabsf(y[i][e].x), fabsf(y[i][e].y)));
             }
-#pragma unroll
-            for (int o = 8; o >= 1; o >>= 1)
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            mine = (int)(threadIdx.x & 15) == i ? amax : mine;
         }
-        const ScalePair sp = group_scale_rule<P2>(mine);
-        if ((threadIdx.x & 15) < CPT) {
-            const int c = (threadIdx.x & ~15) + (threadIdx.x & 15) * blockDim.x;
+        const ScalePair sp = group_scale_rule<P2>(group_max<CPT>(amax));
+        const int mine = (threadIdx.x & 15) / LANES<CPT>;  // this thread's group
+        if ((threadIdx.x & (LANES<CPT> - 1)) == 0 && mine < CPT) {
+            const int c = (threadIdx.x & ~15) + mine * blockDim.x;
             if (c < nchunk)
                 p.scales[(int64_t)(c >> 4) * p.ld_s + t] = sp.s;
         }
 #pragma unroll
         for (int i = 0; i < CPT; ++i) {
             const int c = threadIdx.x + i * blockDim.x;
-            const float2 inv = splat(__shfl_sync(0xffffffffu, sp.inv, (threadIdx.x & 16) + i));
+            const float2 inv = splat(__shfl_sync(0xffffffffu, sp.inv, (threadIdx.x & 16) + i * LANES<CPT>));
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 y[i][e] = __fmul2_rn(y[i][e], inv);
@@ -425,6 +448,7 @@ struct NormBwd {
     float *part;  // [gridDim.x][D]
     int64_t T, lddy, ldh, lddres, lddx;
     int D;
+    float inv_d;
     bool gamma_f32, one_row;  // one_row: per CTA
     int slots;
     int *status;
@@ -524,7 +548,7 @@ __global__ void __launch_bounds__(max_threads(W), min_ctas(W, true)) rmsnorm_bwd
             if (ahead < p.T && !*wc.abort_flag)
                 fetch(ahead, ring.slot, ring.phase ^ 1);
         }
-        const float k = dot / (float)p.D * rstd * rstd;  // dx = rstd * (a - h k)
+        const float k = dot * p.inv_d * rstd * rstd;  // dx = rstd * (a - h k)
 #pragma unroll
         for (int i = 0; i < CPT; ++i) {
             const int c = threadIdx.x + i * blockDim.x;
@@ -727,6 +751,7 @@ extern "C" int fp8_rmsnorm(const void *x, int64_t ldx, const void *residual, int
     p.rstd = rstd;
     p.T = T, p.ldx = ldx, p.ldr = ldr, p.ldh = ldh, p.ldq = ldq, p.ld_s = ld_s;
     p.D = (int)D;
+    p.inv_d = 1.0f / (float)D;
     p.eps = eps;
     p.gamma_f32 = gamma_kind == FP8FG_OUT_F32;
     const RowShape rs = row_shape(D);
@@ -829,6 +854,7 @@ extern "C" int fp8_rmsnorm_bwd(const void *dy, int64_t lddy, const void *h, int6
     p.part = static_cast<float *>(workspace);
     p.T = T, p.lddy = lddy, p.ldh = ldh, p.lddres = lddres, p.lddx = lddx;
     p.D = (int)D;
+    p.inv_d = 1.0f / (float)D;
     p.gamma_f32 = gamma_kind == FP8FG_OUT_F32;
     const RowShape rs = row_shape(D);
     p.slots = ring.slots;
