@@ -705,6 +705,20 @@ int ring_grid(int64_t T, const RingShape &r)
     return (int)(T < cap ? T : (cap > 0 ? cap : 1));
 }
 
+// The backward pass of few rows takes fewer CTAs than fit, since dgamma's second
+// kernel adds up a row from each: two rows each at least, and four CTAs per SM
+// until every one of a full grid has four (us in a graph, 1031 x 2048 without
+// dres: 912 CTAs 10.0, 608 7.8; 300 x 7168: 300 CTAs 9.4, 152 7.2).
+int bwd_grid(int64_t T, RingShape r)
+{
+    const int64_t sms = sm_count() > 0 ? sm_count() : 1;
+    int64_t per_sm = (T + 2 * sms - 1) / (2 * sms);
+    if (T < 4 * sms * r.per_sm)
+        per_sm = std::min<int64_t>(per_sm, 4);
+    r.per_sm = (int)std::min<int64_t>(per_sm, r.per_sm);
+    return ring_grid(T, r);
+}
+
 // (every instantiation may take all of a CTA's shared memory)
 template <auto K, typename P>
 int launch_ring(const P &p, int grid, int threads, size_t smem, cudaStream_t s)
@@ -820,8 +834,11 @@ extern "C" int64_t fp8_rmsnorm_bwd_workspace(int64_t T, int64_t D)
 {
     if (T <= 0 || D <= 0 || !norm_width_ok(D))
         return 0;
-    // the grid is largest without dres and with a bf16 gamma
-    return (int64_t)ring_grid(T, ring_shape(D, 2, false, true)) * D * 4;
+    int grid = 0;
+    for (int tensors = 2; tensors <= 3; ++tensors)
+        for (int f32 = 0; f32 < 2; ++f32)
+            grid = std::max(grid, bwd_grid(T, ring_shape(D, tensors, f32 != 0, true)));
+    return (int64_t)grid * D * 4;
 }
 
 extern "C" int fp8_rmsnorm_bwd(const void *dy, int64_t lddy, const void *h, int64_t ldh, const float *rstd,
@@ -859,7 +876,7 @@ extern "C" int fp8_rmsnorm_bwd(const void *dy, int64_t lddy, const void *h, int6
     if (!device_supported())
         return FP8FG_EUNSUPPORTED;
     const RingShape ring = ring_shape(D, dres ? 3 : 2, gamma_kind == FP8FG_OUT_F32, true);
-    const int grid = ring_grid(T, ring);
+    const int grid = bwd_grid(T, ring);
     if (workspace_bytes < (int64_t)grid * D * 4)
         return FP8FG_EINVAL;
     NormBwd p{};

@@ -166,6 +166,20 @@ def test_backward(T, D, residual, gamma):
     assert torch.equal(again[0], dx) and torch.equal(again[1], dgamma)   # a fixed order of summation
 
 
+@pytest.mark.parametrize("T", [2500, 4900, 7300])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("gamma", ["bf16", "f32"])
+def test_backward_grids(T, residual, gamma):
+    """Lengths where the variants take different numbers of CTAs: the
+    workspace of (T, D) has to cover the largest."""
+    x, r, w = _inputs(T, 1024, seed=T, gamma=gamma)
+    dres = r if residual else None
+    rstd = torch.rand(T, device=DEV) + 0.5
+    dx, dgamma = fg.fp8_rmsnorm_bwd(r, x, rstd, w, dres=dres)
+    assert fg.device_status() == 0
+    _check_bwd(r, x, rstd, w, dres, dx, dgamma)
+
+
 def test_backward_strided_and_in_place():
     T, D = 21, 640
     x, r, w = _inputs(T, 1024, seed=12)
