@@ -94,8 +94,9 @@ def lib():
 
 
 def _checks():
-    """The compiled helper that reads tensors' metadata (raises if it has not
-    been built); it links against torch, so torch comes first."""
+    """The compiled helper that checks and allocates tensors and calls the
+    library with them (raises if it has not been built); it links against
+    torch, so torch comes first."""
     global _helper
     if _helper is None:
         _torch()
@@ -104,6 +105,7 @@ def _checks():
         except ImportError as e:
             raise RuntimeError("_tensors.so is not built for this machine (%s); run `python "
                                "fp8_fine_grained_gb300/build.py` (or __graft_entry__.build()) first" % e)
+        m.bind(lib()._handle)
         _helper = m
     return _helper
 
@@ -603,11 +605,12 @@ def fp8_moe_combine(y, dest, w, out_dtype=None, out=None, stream=None):
 
 # ------------------------------------------- between a gated MLP's GEMMs ----
 # These calls are short (a decoding step spends more time here than on the
-# GPU), so the tensors are checked in the compiled helper: matrix (type, layout,
-# extent; returns the row pitch), vector, and on_gpu last. With a stream of its
-# own a call runs wholly under it: outputs and scratch that the call allocates
-# come from that stream's memory, so that no work still queued on the current
-# stream can be using it.
+# GPU), so the compiled helper checks the tensors (matrix: type, layout, extent;
+# returns the row pitch; vector; on_gpu last), allocates outputs (empty) and
+# calls the library (a tensor stands for its data pointer, None for NULL). With
+# a stream of its own a call runs wholly under it: outputs and scratch that the
+# call allocates come from that stream's memory, so that no work still queued on
+# the current stream can be using it.
 
 def _under(stream, fn, *args, **kw):
     with _torch().cuda.stream(stream):
@@ -630,29 +633,28 @@ def fp8_rmsnorm(x, gamma, eps=1e-6, residual=None, h=None, q=None, scales=None, 
     ldx = H.matrix(x, bf16, 0, 0, "x")
     T, D = x.shape
     kind = H.norm_weight(gamma, D)
-    ldr = ldh = pr = ph = 0
+    ldr = ldh = 0
     if residual is not None:
         ldr = H.matrix(residual, bf16, T, D, "residual")
         if residual.shape != x.shape:
             raise ValueError("residual must be [%d, %d], got %s" % (T, D, tuple(residual.shape)))
         if h is None:
-            h = torch.empty((T, D), dtype=bf16, device=x.device)
+            h = H.empty(x, bf16, T, D)
         ldh = H.matrix(h, bf16, T, D, "h")
-        pr, ph = residual.data_ptr(), h.data_ptr()
     elif h is not None:
         raise ValueError("h is written only with a residual")
     if q is None:
-        q = torch.empty((T, D), dtype=u8, device=x.device)
+        q = H.empty(x, u8, T, D)
     if scales is None:
-        scales = torch.empty((D // 128, _pad(max(T, 1), 4)), dtype=f32, device=x.device)
+        scales = H.empty(x, f32, D // 128, _pad(max(T, 1), 4))
     if rstd is None:
-        rstd = torch.empty(T, dtype=f32, device=x.device)
+        rstd = H.empty(x, f32, T)
     ldq = H.matrix(q, u8, T, D, "q")
     lds = H.matrix(scales, f32, D // 128, T, "scales")
     H.vector(rstd, f32, T, "rstd")
     H.on_gpu(x, "x", gamma, "gamma", residual, "residual", h, "h", q, "q", scales, "scales", rstd, "rstd")
-    rc = lib().fp8_rmsnorm(x.data_ptr(), ldx, pr, ldr, gamma.data_ptr(), kind, T, D, eps, ph, ldh, q.data_ptr(), ldq,
-                           scales.data_ptr(), lds, rstd.data_ptr(), 1 if pow2 else 0, _stream(None))
+    rc = H.fp8_rmsnorm(x, ldx, residual, ldr, gamma, kind, T, D, eps, h, ldh, q, ldq, scales, lds, rstd,
+                       1 if pow2 else 0, _stream(None))
     if rc:
         _check(rc, "fp8_rmsnorm")
     return q, scales, x if h is None else h, rstd
@@ -671,14 +673,13 @@ def fp8_rmsnorm_t(h, rstd, gamma, qT=None, scalesT=None, stream=None, pow2=False
     kind = H.norm_weight(gamma, D)
     H.vector(rstd, f32, T, "rstd")
     if qT is None:
-        qT = torch.empty((D, T), dtype=u8, device=h.device)
+        qT = H.empty(h, u8, D, T)
     if scalesT is None:
-        scalesT = torch.empty((T // 128, _pad(max(D, 1), 4)), dtype=f32, device=h.device)
+        scalesT = H.empty(h, f32, T // 128, _pad(max(D, 1), 4))
     ldq = H.matrix(qT, u8, D, T, "qT")
     lds = H.matrix(scalesT, f32, T // 128, D, "scalesT")
     H.on_gpu(h, "h", rstd, "rstd", gamma, "gamma", qT, "qT", scalesT, "scalesT")
-    rc = lib().fp8_rmsnorm_t(h.data_ptr(), ldh, rstd.data_ptr(), gamma.data_ptr(), kind, T, D, qT.data_ptr(), ldq,
-                             scalesT.data_ptr(), lds, 1 if pow2 else 0, _stream(None))
+    rc = H.fp8_rmsnorm_t(h, ldh, rstd, gamma, kind, T, D, qT, ldq, scalesT, lds, 1 if pow2 else 0, _stream(None))
     if rc:
         _check(rc, "fp8_rmsnorm_t")
     return qT, scalesT
@@ -699,21 +700,17 @@ def fp8_rmsnorm_bwd(dy, h, rstd, gamma, dres=None, dx=None, dgamma=None, stream=
     ldh = H.matrix(h, bf16, T, D, "h")
     H.vector(rstd, f32, T, "rstd")
     kind = H.norm_weight(gamma, D)
-    lddres = pdres = 0
-    if dres is not None:
-        lddres, pdres = H.matrix(dres, bf16, T, D, "dres"), dres.data_ptr()
+    lddres = H.matrix(dres, bf16, T, D, "dres") if dres is not None else 0
     if dx is None:
-        dx = torch.empty((T, D), dtype=bf16, device=dy.device)
+        dx = H.empty(dy, bf16, T, D)
     if dgamma is None:
-        dgamma = torch.empty(D, dtype=f32, device=dy.device)
+        dgamma = H.empty(dy, f32, D)
     lddx = H.matrix(dx, bf16, T, D, "dx")
     H.vector(dgamma, f32, D, "dgamma")
     H.on_gpu(dy, "dy", h, "h", rstd, "rstd", gamma, "gamma", dres, "dres", dx, "dx", dgamma, "dgamma")
-    L = lib()
-    nbytes = L.fp8_rmsnorm_bwd_workspace(T, D)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dy.device)
-    rc = L.fp8_rmsnorm_bwd(dy.data_ptr(), lddy, h.data_ptr(), ldh, rstd.data_ptr(), gamma.data_ptr(), kind, pdres,
-                           lddres, T, D, dx.data_ptr(), lddx, dgamma.data_ptr(), ws.data_ptr(), nbytes,
+    nbytes = H.fp8_rmsnorm_bwd_workspace(T, D)
+    ws = H.empty(dy, torch.uint8, nbytes)
+    rc = H.fp8_rmsnorm_bwd(dy, lddy, h, ldh, rstd, gamma, kind, dres, lddres, T, D, dx, lddx, dgamma, ws, nbytes,
                            _stream(None))
     if rc:
         _check(rc, "fp8_rmsnorm_bwd")
@@ -746,19 +743,17 @@ def fp8_gated_gemm(xq, sx, wq, sw, h=None, scales=None, gu=None, save=False, str
         raise ValueError("sw must be a contiguous float32 [%d, %d], got %s %s"
                          % (N2 // 128, K // 128, sw.dtype, tuple(sw.shape)))
     if h is None:
-        h = torch.empty((M, I), dtype=u8, device=xq.device)
+        h = H.empty(xq, u8, M, I)
     if scales is None:
-        scales = torch.empty((I // 128, _pad(max(M, 1), 4)), dtype=f32, device=xq.device)
+        scales = H.empty(xq, f32, I // 128, _pad(max(M, 1), 4))
     if gu is None and save:
-        gu = torch.empty((M, N2), dtype=torch.bfloat16, device=xq.device)
+        gu = H.empty(xq, torch.bfloat16, M, N2)
     ldh = H.matrix(h, u8, M, I, "h")
     lds = H.matrix(scales, f32, I // 128, M, "scales")
-    ldgu = pgu = 0
-    if gu is not None:
-        ldgu, pgu = H.matrix(gu, torch.bfloat16, M, N2, "gu"), gu.data_ptr()
+    ldgu = H.matrix(gu, torch.bfloat16, M, N2, "gu") if gu is not None else 0
     H.on_gpu(xq, "xq", sx, "sx", wq, "wq", sw, "sw", h, "h", scales, "scales", gu, "gu")
-    rc = lib().fp8_gated_gemm(xq.data_ptr(), sx.data_ptr(), ldx, ldsx, wq.data_ptr(), sw.data_ptr(), ldw, M, I, K,
-                              h.data_ptr(), ldh, scales.data_ptr(), lds, pgu, ldgu, 1 if pow2 else 0, _stream(None))
+    rc = H.fp8_gated_gemm(xq, sx, ldx, ldsx, wq, sw, ldw, M, I, K, h, ldh, scales, lds, gu, ldgu, 1 if pow2 else 0,
+                          _stream(None))
     if rc:
         _check(rc, "fp8_gated_gemm")
     return h, scales, gu
@@ -781,27 +776,25 @@ def fp8_gated_bwd(gu, dh, q=None, scales=None, qT=None, scalesT=None, hqT=None, 
     M, I = dh.shape
     if gu.shape != (M, 2 * I):
         raise ValueError("gu must be [%d, %d], got %s" % (M, 2 * I, tuple(gu.shape)))
-    dev = dh.device
     if q is None:
-        q = torch.empty((M, 2 * I), dtype=u8, device=dev)
+        q = H.empty(dh, u8, M, 2 * I)
     if scales is None:
-        scales = torch.empty((2 * I // 128, _pad(max(M, 1), 4)), dtype=f32, device=dev)
+        scales = H.empty(dh, f32, 2 * I // 128, _pad(max(M, 1), 4))
     if qT is None:
-        qT = torch.empty((2 * I, M), dtype=u8, device=dev)
+        qT = H.empty(dh, u8, 2 * I, M)
     if scalesT is None:
-        scalesT = torch.empty((M // 128, _pad(max(2 * I, 1), 4)), dtype=f32, device=dev)
+        scalesT = H.empty(dh, f32, M // 128, _pad(max(2 * I, 1), 4))
     if hqT is None:
-        hqT = torch.empty((I, M), dtype=u8, device=dev)
+        hqT = H.empty(dh, u8, I, M)
     if hscalesT is None:
-        hscalesT = torch.empty((M // 128, _pad(max(I, 1), 4)), dtype=f32, device=dev)
+        hscalesT = H.empty(dh, f32, M // 128, _pad(max(I, 1), 4))
     ldq, lds = H.matrix(q, u8, M, 2 * I, "q"), H.matrix(scales, f32, 2 * I // 128, M, "scales")
     ldqT, ldsT = H.matrix(qT, u8, 2 * I, M, "qT"), H.matrix(scalesT, f32, M // 128, 2 * I, "scalesT")
     ldhT, ldhs = H.matrix(hqT, u8, I, M, "hqT"), H.matrix(hscalesT, f32, M // 128, I, "hscalesT")
     H.on_gpu(gu, "gu", dh, "dh", q, "q", scales, "scales", qT, "qT", scalesT, "scalesT", hqT, "hqT", hscalesT,
              "hscalesT")
-    rc = lib().fp8_gated_bwd(gu.data_ptr(), ldgu, dh.data_ptr(), lddh, M, I, q.data_ptr(), ldq, scales.data_ptr(), lds,
-                             qT.data_ptr(), ldqT, scalesT.data_ptr(), ldsT, hqT.data_ptr(), ldhT, hscalesT.data_ptr(),
-                             ldhs, 1 if pow2 else 0, _stream(None))
+    rc = H.fp8_gated_bwd(gu, ldgu, dh, lddh, M, I, q, ldq, scales, lds, qT, ldqT, scalesT, ldsT, hqT, ldhT, hscalesT,
+                         ldhs, 1 if pow2 else 0, _stream(None))
     if rc:
         _check(rc, "fp8_gated_bwd")
     return q, scales, qT, scalesT, hqT, hscalesT
@@ -827,14 +820,12 @@ def grad_clip(grads, max_norm, eps=1e-6, out=None, norm=None, stream=None):
         raise ValueError("grads must hold at least one tensor")
     table = H.describe(grads, outs)
     if norm is None:
-        norm = torch.empty(2, dtype=torch.float32, device=grads[0].device)
+        norm = H.empty(grads[0], torch.float32, 2)
     H.vector(norm, torch.float32, 2, "norm")
     H.on_gpu(grads[0], "grads", norm, "norm")
-    L = lib()
-    nbytes = L.fp8fg_grad_clip_workspace(n)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=norm.device)
-    rc = L.fp8fg_grad_clip(table, n, max_norm, eps, norm.data_ptr(), ws.data_ptr(), nbytes,
-                           _stream(None))
+    nbytes = H.fp8fg_grad_clip_workspace(n)
+    ws = H.empty(norm, torch.uint8, nbytes)
+    rc = H.fp8fg_grad_clip(table, n, max_norm, eps, norm, ws, nbytes, _stream(None))
     if rc:
         _check(rc, "fp8fg_grad_clip")
     return norm, outs

@@ -1,18 +1,27 @@
-// CPython helper of the binding: the argument checks of its short calls, and
-// the table that fp8fg_grad_clip reads, from torch tensors.
+// CPython helper of the binding: the argument checks of its short calls, their
+// outputs' allocation, the calls themselves, and the table that fp8fg_grad_clip
+// reads, from torch tensors.
 //
 // Looking at one property of a tensor from Python takes 0.07 to 0.15 us, a
-// check of its type, layout and extent half a microsecond with the call: for a
-// decoding step's norm that was more than the kernel, and for the gradients of
-// a whole model many times the library's own work. Here it takes a few
-// nanoseconds. This module only reads the tensors' metadata; it is compiled
-// against the installed torch.
+// check of its type, layout and extent half a microsecond with the call, a
+// foreign call with 18 arguments 1.5 us: for a decoding step's norm that was
+// more than the kernel, and for the gradients of a whole model many times the
+// library's own work. Here it takes a few nanoseconds. A norm of one row takes
+// 3.8 us in all (6.2 by ctypes), half of it the launch, and its four outputs 6
+// more (15 by torch.empty). This module is compiled against the installed
+// torch.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+#include <dlfcn.h>
 
 #include <exception>
+#include <tuple>
+#include <type_traits>
+#include <utility>
 
+#include <ATen/ops/empty.h>
 #include <torch/csrc/Dtype.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "fp8fg.h"
@@ -195,6 +204,101 @@ PyObject *on_gpu(PyObject *, PyObject *const *args, Py_ssize_t nargs)
     });
 }
 
+// empty(like, dtype, n) or empty(like, dtype, rows, cols) -> a contiguous
+// tensor on like's device
+PyObject *empty(PyObject *, PyObject *const *args, Py_ssize_t nargs)
+{
+    HANDLE_TH_ERRORS  // (out of memory stays torch's own error)
+    if ((nargs != 3 && nargs != 4) || !THPVariable_Check(args[0]) || !THPDtype_Check(args[1]))
+        return refuse("bad call of the allocation");
+    int64_t size[2] = {0, 0};
+    for (Py_ssize_t i = 2; i < nargs; ++i)
+        size[i - 2] = PyLong_AsLongLong(args[i]);
+    if (PyErr_Occurred())
+        return nullptr;
+    const at::TensorOptions options = at::TensorOptions()
+                                          .dtype(reinterpret_cast<THPDtype *>(args[1])->scalar_type)
+                                          .device(THPVariable_Unpack(args[0]).device());
+    return THPVariable_Wrap(at::empty(at::IntArrayRef(size, (size_t)nargs - 2), options));
+    END_HANDLE_TH_ERRORS
+}
+
+// An argument of a library call: pointers come from a tensor (its data), None,
+// a bytes object or an address.
+template <typename T>
+bool take(PyObject *o, T &v)
+{
+    if constexpr (std::is_pointer_v<T>) {
+        if (THPVariable_Check(o)) {
+            const at::Tensor &t = THPVariable_Unpack(o);
+            if constexpr (std::is_const_v<std::remove_pointer_t<T>>)
+                v = static_cast<T>(t.const_data_ptr());
+            else
+                v = static_cast<T>(t.mutable_data_ptr());
+        } else if (o == Py_None) {
+            v = nullptr;
+        } else if (PyBytes_Check(o)) {
+            v = reinterpret_cast<T>(PyBytes_AS_STRING(o));
+        } else {
+            v = static_cast<T>(PyLong_AsVoidPtr(o));
+        }
+    } else if constexpr (std::is_floating_point_v<T>) {
+        v = (T)PyFloat_AsDouble(o);
+    } else {
+        v = (T)PyLong_AsLongLong(o);
+    }
+    return !PyErr_Occurred();
+}
+
+template <typename R, typename... A, size_t... I>
+PyObject *invoke(R (*fn)(A...), PyObject *const *args, Py_ssize_t nargs, std::index_sequence<I...>)
+{
+    if (!fn || nargs != (Py_ssize_t)sizeof...(A))
+        return refuse(fn ? "bad call of the library" : "the library is not bound");
+    return guarded([&]() -> PyObject * {
+        std::tuple<A...> v;
+        if (!(take(args[I], std::get<I>(v)) && ...))
+            return nullptr;
+        R r;
+        Py_BEGIN_ALLOW_THREADS;  // (a launch waits when the stream's queue is full)
+        r = fn(std::get<I>(v)...);
+        Py_END_ALLOW_THREADS;
+        return PyLong_FromLongLong(r);
+    });
+}
+
+template <typename R, typename... A>
+PyObject *invoke(R (*fn)(A...), PyObject *const *args, Py_ssize_t nargs)
+{
+    return invoke(fn, args, nargs, std::index_sequence_for<A...>());
+}
+
+// NAME(arguments of the library's NAME) -> what it returns
+#define ENTRIES(X) \
+    X(fp8_rmsnorm) X(fp8_rmsnorm_t) X(fp8_rmsnorm_bwd) X(fp8_rmsnorm_bwd_workspace) X(fp8_gated_gemm) \
+    X(fp8_gated_bwd) X(fp8fg_grad_clip) X(fp8fg_grad_clip_workspace)
+#define DEFINE(NAME) \
+    decltype(&::NAME) NAME##_fn; \
+    PyObject *call_##NAME(PyObject *, PyObject *const *args, Py_ssize_t nargs) \
+    { \
+        return invoke(NAME##_fn, args, nargs); \
+    }
+ENTRIES(DEFINE)
+
+// bind(handle): look the entry points up in the loaded library
+PyObject *bind(PyObject *, PyObject *handle)
+{
+    void *lib = PyLong_AsVoidPtr(handle);
+    if (PyErr_Occurred())
+        return nullptr;
+#define LOOKUP(NAME) \
+    NAME##_fn = reinterpret_cast<decltype(&::NAME)>(dlsym(lib, #NAME)); \
+    if (!NAME##_fn) \
+        return refuse("the library lacks " #NAME);
+    ENTRIES(LOOKUP)
+    Py_RETURN_NONE;
+}
+
 template <typename F>
 PyCFunction fast(F f) { return reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(f)); }
 
@@ -204,6 +308,10 @@ PyMethodDef methods[] = {
     {"vector", fast(vector), METH_FASTCALL, "vector(t, dtype, n, name)"},
     {"norm_weight", fast(norm_weight), METH_FASTCALL, "norm_weight(gamma, D) -> output kind of its type"},
     {"on_gpu", fast(on_gpu), METH_FASTCALL, "on_gpu(t, name, t, name, ...)"},
+    {"empty", fast(empty), METH_FASTCALL, "empty(like, dtype, n) or (like, dtype, rows, cols) -> tensor"},
+    {"bind", bind, METH_O, "bind(handle of libfp8fg.so)"},
+#define METHOD(NAME) {#NAME, fast(call_##NAME), METH_FASTCALL, #NAME "(the library's arguments) -> what it returns"},
+    ENTRIES(METHOD)
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

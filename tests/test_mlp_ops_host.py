@@ -293,3 +293,34 @@ def test_tensor_table():
     with pytest.raises(ValueError, match="contiguous"):
         _tensors.describe([flat[::2]], [flat[:10]])
     assert _tensors.describe([], []) == b""
+
+
+def test_library_calls_of_the_helper():
+    """The helper's calls: a tensor is its data pointer, None is NULL, and the
+    library's own refusals come back as its status codes."""
+    H = fg._checks()
+    x = torch.zeros(2, 128, dtype=BF16)
+    with pytest.raises(ValueError, match="bad call of the library"):
+        H.fp8_rmsnorm(x, 128)
+    with pytest.raises(TypeError):
+        H.fp8_rmsnorm_t(x, 128, x, x, "1", 2, 128, x, 2, x, 128, 0, 0)
+    with pytest.raises(TypeError):
+        H.fp8_rmsnorm_t(object(), 128, x, x, 1, 2, 128, x, 2, x, 128, 0, 0)
+    ok, einval = 0, fg.lib().fp8_rmsnorm_t(0, 128, 0, 0, 1, 3, 128, 0, 128, 0, 128, 0, 0)    # 3 rows
+    assert einval != ok
+    assert H.fp8_rmsnorm_t(x, 128, x, x, 1, 3, 128, x, 128, x, 128, 0, 0) == einval
+    assert H.fp8_rmsnorm_t(None, 128, None, None, 1, 128, 128, None, 128, None, 128, 0, 0) == einval   # NULL
+    assert H.fp8_rmsnorm_t(None, 128, None, None, 1, 0, 128, None, 0, None, 128, 0, 0) == ok            # no rows
+
+
+def test_allocation_of_the_helper():
+    H = fg._checks()
+    x = torch.zeros(3)
+    a, b = H.empty(x, U8, 5), H.empty(x, BF16, 5, 6)
+    assert a.shape == (5,) and a.dtype is U8 and b.shape == (5, 6) and b.dtype is BF16 and b.is_contiguous()
+    assert H.empty(x, F32, 0, 4).shape == (0, 4)
+    for args in ((x, U8), (x, 3, 1), (3, U8, 1), (x, U8, 1, 1, 1)):
+        with pytest.raises(ValueError, match="bad call"):
+            H.empty(*args)
+    with pytest.raises(RuntimeError, match="negative"):
+        H.empty(x, U8, -1)
