@@ -6,7 +6,7 @@
 //   out  = g * coef
 //
 // Two streams over the data: the norm has to be known before the first
-// element is written. 400 M FP32 elements take 730 us (4.8 GB, 6.6 TB/s or 0.97
+// element is written. 400 M FP32 elements take 723 us (4.8 GB, 6.6 TB/s or 0.98
 // of the measured copy). The first kernel leaves one FP64 partial sum per CTA;
 // every CTA of the second adds those up in the same order (a few KB from L2),
 // so the result does not depend on the schedule and no third launch is needed.
@@ -16,15 +16,16 @@
 // The tensors' pointers and sizes travel in the kernels' parameters (no device
 // table to copy). A tensor is cut into chunks of bytes whose vector loads start
 // on a 16-byte boundary of its own; the elements before the first boundary
-// belong to chunk 0. Chunks are dealt round-robin to the CTAs. Both kernels run
-// best with few CTAs that each keep a whole chunk in flight (UNROLL 16-byte
-// loads per thread): 400 M FP32 elements, us, with chunks of
-//   64 KB (sums) and 32 KB (scaling): 725 with 2 CTAs per SM, 738 with 3
-//   32 KB and 32 KB:                  722 with 2, 752 with 4
-//   64 KB and 64 KB:                  744 with 2
-//   32 KB and 16 KB:                  783 with 4
-// and a short list (1.5 M elements) takes 10.2 with the first, 11.1 with the
-// second.
+// belong to chunk 0. Chunks are dealt round-robin to the CTAs, a whole chunk in
+// flight in each (UNROLL 16-byte loads per thread). CTAs per SM of the sums and
+// of the scaling, with chunks of 64 and 32 KB, us in a loop of calls:
+//                              2, 2    3, 2    2, 3    3, 3
+//   400 M FP32 elements         744     734     778     763
+//   30 M, in 120 tensors       63.3    63.1    59.2    59.1
+//   1.5 M, in 120 tensors      10.9     9.5     9.6     9.5
+// so the scaling takes 3 up to 256 MB (what the sums leave in L2 is then still a
+// good part of it) and 2 beyond. Other chunks for 400 M: 32 and 32 KB 776, 32
+// and 16 KB 777, 64 and 64 KB 760.
 #include <cuda_bf16.h>
 
 #include "host_common.h"
@@ -34,7 +35,8 @@ namespace fp8fg {
 namespace {
 
 constexpr int THREADS = 256;
-constexpr int CTAS_PER_SM = 2;
+constexpr int CTAS_PER_SM = 3;
+constexpr int64_t SCALE_WIDE_BYTES = 256ll << 20;  // the scaling's third CTA up to here
 constexpr int SUM_UNROLL = 16, SCALE_UNROLL = 8;
 constexpr int chunk_bytes(int unroll) { return unroll * THREADS * 16; }
 constexpr int MAX_TENSORS = 1024;  // per launch: 24 bytes + 4 each in the 32 KB of kernel parameters
@@ -272,15 +274,15 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
 }
 
 // CTAs of a launch: all resident at once.
-int64_t grid_cap()
+int64_t grid_cap(int per_sm)
 {
     const int sms = sm_count();
-    return (int64_t)(sms > 0 ? sms : 1) * CTAS_PER_SM;
+    return (int64_t)(sms > 0 ? sms : 1) * per_sm;
 }
 
-unsigned grid_of(int64_t chunks)
+unsigned grid_of(int64_t chunks, int per_sm)
 {
-    const int64_t cap = grid_cap();
+    const int64_t cap = grid_cap(per_sm);
     return (unsigned)(chunks < cap ? (chunks > 0 ? chunks : 1) : cap);
 }
 
@@ -315,7 +317,7 @@ int launch_sumsq(const fp8fg_grad *t, int take, double *partial, int *used, cuda
 {
     Table<N> tab;
     fill(tab, t, take, SUM_UNROLL);
-    const unsigned grid = grid_of(tab.first[take]);
+    const unsigned grid = grid_of(tab.first[take], CTAS_PER_SM);
     *used = (int)grid;
     return launch_pss(sumsq_kernel<N>, dim3(grid), THREADS, 0, s, tab, partial);
 }
@@ -326,8 +328,9 @@ int launch_scale(const fp8fg_grad *t, int take, const double *partial, int n_par
 {
     Table<N> tab;
     fill(tab, t, take, SCALE_UNROLL);
-    return launch_pss(scale_kernel<N>, dim3(grid_of(tab.first[take])), THREADS, 0, s, tab, partial, n_partial, max_norm,
-                      eps, norm);
+    const int64_t chunks = tab.first[take];
+    const unsigned grid = grid_of(chunks, chunks * chunk_bytes(SCALE_UNROLL) <= SCALE_WIDE_BYTES ? CTAS_PER_SM : 2);
+    return launch_pss(scale_kernel<N>, dim3(grid), THREADS, 0, s, tab, partial, n_partial, max_norm, eps, norm);
 }
 
 }  // namespace
@@ -340,7 +343,7 @@ extern "C" int64_t fp8fg_grad_clip_workspace(int64_t count)
     if (count < 0)
         return 0;
     const int64_t launches = count > 0 ? (count + MAX_TENSORS - 1) / MAX_TENSORS : 1;
-    return launches * grid_cap() * 8;
+    return launches * grid_cap(CTAS_PER_SM) * 8;
 }
 
 extern "C" int fp8fg_grad_clip(const fp8fg_grad *grads, int64_t count, float max_norm, float eps, float *norm,
