@@ -174,10 +174,10 @@ constexpr int MAX_SLOTS = 3;
 constexpr uint32_t BAR_BYTES = (8 * MAX_SLOTS + 15) / 16 * 16;  // (gamma follows)
 
 // Where gamma is staged in shared memory: in the backward pass, which reads it
-// twice per row, and in the forward pass without a residual (8192 x 7168: 39 us,
-// from global memory 42). With a residual the loads from global memory are
-// moved over the reduction's barrier and the space serves the ring better (65
-// us, staged 72). The widest rows need the space for their second slot.
+// twice per row, and in the forward pass without a residual (8192 x 7168: 34.5
+// us, from global memory 36.6). With a residual the loads from global memory
+// are moved over the reduction's barrier and the space serves L1 better (63.7
+// us, staged 70.2). The widest rows need the space for their second slot.
 constexpr bool stages_gamma(int w, bool bwd, int tensors) { return w != WIDE && (bwd || tensors == 1); }
 
 __device__ __forceinline__ void stage_gamma(uint8_t *dst, const void *gamma, uint32_t bytes)
@@ -238,10 +238,11 @@ struct NormFwd {
     uint64_t wait_limit_ns;
 };
 
-// 7 bytes per element with a residual: 8191 x 7168 in 65 us, 6.3 TB/s or 0.93
-// of the measured copy, 4096 x 18432 in 80 us (0.97). Without one (3 bytes) it
-// is bound by issue and latency, 122 warp instructions per 256 elements: 8192 x
-// 7168 in 38.5 us, 0.67.
+// 7 bytes per element with a residual: 8191 x 7168 in 63.4 us, 6.5 TB/s or 0.96
+// of the measured copy, 4096 x 18432 in 85 us (0.91). Without one (3 bytes) it
+// is bound by issue and latency, 110 warp instructions per 256 elements: 8192 x
+// 7168 in 34.5 us, 0.75; with one CTA more per SM (at 64 registers) narrow rows
+// gained nothing and 5120 columns went from 33 us to 35.
 //
 // One row per CTA at a time: thread t owns chunks t, t + blockDim, ...; a
 // half-warp's 16 chunks are one 128-column group (D % 128 == 0 and blockDim
@@ -473,9 +474,9 @@ struct NormBwd {
     uint64_t wait_limit_ns;
 };
 
-// 8 bytes per element with dres: 8192 x 7168 in 75.2 us with the reduction of
-// dgamma (about 5 us of it), 6.2 TB/s or 0.92 of the measured copy; 6 bytes
-// without: 60.8 us, 0.85.
+// 8 bytes per element with dres: 8192 x 7168 in 74.5 us with the reduction of
+// dgamma (about 4 us of it), 6.3 TB/s or 0.93 of the measured copy; 6 bytes
+// without: 57.7 us, 0.90.
 //
 // The thread's columns are the same in every row, so its dgamma terms add up
 // in registers and leave once, as the CTA's row of `part`.
@@ -483,7 +484,7 @@ struct NormBwd {
 // depend on the schedule. The row's values go from the ring to registers as
 // they are (bf16), so that the slot can be refilled under the second half of
 // the row's work: with two slots a CTA then always has two rows in flight
-// (8192 x 7168 with dres 75.9 us; 87 when the row was read from the ring
+// (8192 x 7168 with dres 74.5 us; 87 when the row was read from the ring
 // twice and held its slot).
 template <int W, bool RES>
 __global__ void __launch_bounds__(max_threads(W), min_ctas(W, true)) rmsnorm_bwd_kernel(const NormBwd p)

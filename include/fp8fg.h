@@ -563,11 +563,10 @@ FP8FG_API int fp8_gated_bwd(const void *gu, int64_t ldgu, const void *dh, int64_
  *   workspace  8-byte aligned, at least fp8fg_grad_clip_workspace(count)
  *           bytes on the current device.
  *   Squares are FP32 and are added up in FP32 inside a thread's part of 64 KB
- *   (sums 16 terms deep), in FP64 beyond; the order is fixed, so the result
- *   does not vary
- *   between calls. Elements beyond 1.8e19 in magnitude give an infinite norm
- *   (coef 0), a NaN gives NaN everywhere; elements below 1e-23 count as zero
- *   in the norm.
+ *   (four sums of pairs, up to 130 squares in all), in FP64 beyond; the order is
+ *   fixed, so the result does not vary between calls. Elements beyond 1.6e18
+ *   in magnitude may give an infinite norm (coef 0), a NaN gives NaN
+ *   everywhere; elements below 1e-23 count as zero in the norm.
  *   max_norm >= 0, eps >= 0.
  * ------------------------------------------------------------------- */
 typedef struct {
