@@ -94,6 +94,9 @@ __device__ __forceinline__ Piece piece_of(const Table<N> &tab, uint32_t chunk, i
     return q;
 }
 
+// (The kernels here may start before the stream's previous kernel ends: nothing
+// is read by the read-only path, which promises data that does not change while
+// the grid runs.)
 __device__ __forceinline__ float load_one(const uint8_t *p, int64_t i, bool bf16)
 {
     return bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p)[i])
@@ -219,7 +222,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
 
 template <int N>
 __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
-    scale_kernel(const __grid_constant__ Table<N> tab, const double *__restrict__ partial, int n_partial,
+    scale_kernel(const __grid_constant__ Table<N> tab, const double *partial, int n_partial,
                  float max_norm, float eps, float *norm_out)
 {
     griddep_wait();

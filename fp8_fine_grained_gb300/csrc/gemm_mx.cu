@@ -369,6 +369,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         };
         seek();
         auto load_sf = [&]() -> Sf {
+            // (plain loads: the grid may have started before the kernel that
+            // wrote the scales ended, so the read-only path is not for them)
             Sf v;
             v.a = 1.0f;
 #pragma unroll
@@ -379,13 +381,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const int kb = ckb;
             const int64_t row = cm0 + quarter * 32 + lane;
             if (row < crow_end)
-                v.a = __ldg(p.sA + (int64_t)kb * p.ld_sA + row);
+                v.a = p.sA[(int64_t)kb * p.ld_sA + row];
             if constexpr (MODE == WGRAD) {
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     const int64_t n = cn0 + 32 * c + lane;
                     if (n < p.N)
-                        v.b[c] = __ldg(p.sB + (int64_t)kb * p.ld_sB + n);
+                        v.b[c] = p.sB[(int64_t)kb * p.ld_sB + n];
                 }
             } else {
 #pragma unroll
@@ -393,10 +395,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     const int64_t nb = cn0 / 128 + h;
                     if (nb * 128 < p.N) {
                         if constexpr (MODE == GROUPED_C)  // expert block scales [E][N/128][K/128]
-                            v.b[h] = __ldg(p.sB + ((int64_t)cexp * (p.N / 128) + nb) * p.ld_sB + kb);
+                            v.b[h] = p.sB[((int64_t)cexp * (p.N / 128) + nb) * p.ld_sB + kb];
                         else
-                            v.b[h] = MODE == FPROP ? __ldg(p.sB + nb * p.ld_sB + kb)
-                                                   : __ldg(p.sB + (int64_t)kb * p.ld_sB + nb);
+                            v.b[h] = MODE == FPROP ? p.sB[nb * p.ld_sB + kb]
+                                                   : p.sB[(int64_t)kb * p.ld_sB + nb];
                     }
                 }
             }

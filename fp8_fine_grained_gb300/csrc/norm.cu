@@ -44,7 +44,10 @@ constexpr int cpt_of(int w) { return w == ONE ? 1 : (w == TWO ? 2 : (w == FOUR ?
 constexpr int max_threads(int w) { return w < FOUR ? 32 : (w == FOUR ? 256 : 768); }
 constexpr int min_ctas(int w, bool bwd) { return w < FOUR ? (bwd ? 12 : 28) : (w == FOUR ? (bwd ? 2 : 3) : 1); }
 
-// (not the read-only path: the outputs may be the inputs' own buffers)
+// Every kernel here may start before the stream's previous kernel ends, so what
+// that kernel may have written is read after griddep_wait and never by the
+// read-only path (__ldg, const __restrict__), which promises data that does not
+// change while the grid runs. (The outputs may be the inputs' own buffers, too.)
 __device__ __forceinline__ uint4 ld_stream(const uint16_t *p)
 {
     uint4 v;
@@ -375,10 +378,9 @@ __global__ void __launch_bounds__(max_threads(W), min_ctas(W, false)) rmsnorm_fw
 constexpr int NT_COLS = 64;
 
 template <bool P2>
-__global__ void __launch_bounds__(256, 5) rmsnorm_t_kernel(const uint16_t *__restrict__ h, int64_t ldh,
-                                                           const float *__restrict__ rstd, const void *gamma,
-                                                           bool gamma_f32, int64_t cols, uint8_t *__restrict__ qT,
-                                                           int64_t ldq, float *__restrict__ scales, int64_t ld_s)
+__global__ void __launch_bounds__(256, 5) rmsnorm_t_kernel(const uint16_t *h, int64_t ldh, const float *rstd,
+                                                           const void *gamma, bool gamma_f32, int64_t cols,
+                                                           uint8_t *qT, int64_t ldq, float *scales, int64_t ld_s)
 {
     griddep_launch_dependents();
     griddep_wait();
@@ -533,9 +535,9 @@ __global__ void __launch_bounds__(max_threads(W), min_ctas(W, true)) rmsnorm_bwd
         for (int e = 0; e < 4; ++e)
             dg[i][e] = splat(0.0f);
     int b = 0;
-    float rstd = blockIdx.x < p.T ? __ldg(p.rstd + blockIdx.x) : 0.0f;
+    float rstd = blockIdx.x < p.T ? p.rstd[blockIdx.x] : 0.0f;
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, b ^= 1, ring.next()) {
-        const float rstd_next = t + gridDim.x < p.T ? __ldg(p.rstd + t + gridDim.x) : 0.0f;
+        const float rstd_next = t + gridDim.x < p.T ? p.rstd[t + gridDim.x] : 0.0f;
         mbar_wait(ring.bar(), ring.phase, wc, FP8FG_ETIMEOUT);
         const uint32_t src = ring.base + ring.slot * ring.slot_bytes;
         uint4 dv[CPT], hv[CPT], rv[CPT];
@@ -615,8 +617,8 @@ __global__ void __launch_bounds__(max_threads(W), min_ctas(W, true)) rmsnorm_bwd
 constexpr int DG_SLICES = 64;
 constexpr int DG_THREADS = 8 * DG_SLICES;
 
-__global__ void __launch_bounds__(DG_THREADS) norm_dgamma_kernel(const float4 *__restrict__ part, int rows, int D,
-                                                                 float *__restrict__ dgamma)
+__global__ void __launch_bounds__(DG_THREADS) norm_dgamma_kernel(const float4 *part, int rows, int D,
+                                                                 float *dgamma)
 {
     griddep_wait();
     __shared__ float4 s[DG_SLICES][8];
@@ -626,7 +628,7 @@ __global__ void __launch_bounds__(DG_THREADS) norm_dgamma_kernel(const float4 *_
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
     for (int r = slice; r < rows; r += DG_SLICES) {
-        const float4 a = __ldg(col + (int64_t)r * (D / 4));
+        const float4 a = col[(int64_t)r * (D / 4)];
         v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
     }
     s[slice][c4] = v;
