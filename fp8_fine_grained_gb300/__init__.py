@@ -610,7 +610,8 @@ def fp8_moe_combine(y, dest, w, out_dtype=None, out=None, stream=None):
 # calls the library (a tensor stands for its data pointer, None for NULL). With
 # a stream of its own a call runs wholly under it: outputs and scratch that the
 # call allocates come from that stream's memory, so that no work still queued on
-# the current stream can be using it.
+# the current stream can be using it. The tensors live on the current device
+# (on the stream's, with a stream); on_gpu refuses others.
 
 def _under(stream, fn, *args, **kw):
     with _torch().cuda.stream(stream):

@@ -20,6 +20,7 @@
 #include <utility>
 
 #include <ATen/ops/empty.h>
+#include <c10/core/impl/DeviceGuardImplInterface.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -184,7 +185,8 @@ PyObject *norm_weight(PyObject *, PyObject *const *args, Py_ssize_t nargs)
 }
 
 // on_gpu(t, name, t, name, ...): every tensor (None is skipped) is a CUDA
-// tensor, all on one device
+// tensor, all on one device, and that is the current one: the call's stream,
+// its workspace's size and its launch are the current device's
 PyObject *on_gpu(PyObject *, PyObject *const *args, Py_ssize_t nargs)
 {
     return guarded([&]() -> PyObject * {
@@ -199,6 +201,12 @@ PyObject *on_gpu(PyObject *, PyObject *const *args, Py_ssize_t nargs)
                 device = d;
             if (d != device)
                 return PyErr_Format(PyExc_ValueError, "%U must be on the other tensors' device", args[i + 1]);
+        }
+        if (!device.is_cpu()) {
+            const int current = c10::impl::getDeviceGuardImpl(device.type())->getDevice().index();
+            if (device.index() != current)
+                return PyErr_Format(PyExc_ValueError, "the tensors must be on the current device (cuda:%d), not on cuda:%d",
+                                    current, (int)device.index());
         }
         Py_RETURN_NONE;
     });
