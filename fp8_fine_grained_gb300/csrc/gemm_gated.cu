@@ -44,6 +44,7 @@
 #include "gated_args.h"
 #include "group_rule.cuh"
 #include "host_common.h"
+#include "per_device.h"
 #include "ptx.cuh"
 #include "tensor_map.h"
 
@@ -504,27 +505,26 @@ bool set_attributes()
     return allow_smem(gated_cluster_kernel<TILING>, Shape<TILING>::total, done);
 }
 
-// Clusters of `split` CTAs that run at once. A cluster's CTAs share a GPC, so
-// this is less than SMs / split; asked once per tiling and split and kept for
-// the process (0: not yet asked), since it only steers the choice of a tiling.
+// Clusters of `split` CTAs that run at once on device `dev` (the current one);
+// 0 when the query fails. A cluster's CTAs share a GPC, so this is less than
+// SMs / split; asked once per device, tiling and split.
 template <int TILING>
-int clusters_at_once(int split)
+int clusters_at_once(int dev, int split)
 {
-    static std::atomic<int> known[MAX_SPLIT + 1];
-    int n = known[split].load();
-    if (n == 0) {
+    static PerDevice known[MAX_SPLIT + 1];
+    return known[split].get(dev, [&] {
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[2];
         launch_config<TILING>(cfg, attr, sm_count(), split, nullptr);
         cfg.numAttrs = 1;  // the cluster dimension
+        int n = 0;
         if (!set_attributes<TILING>() ||
-            cudaOccupancyMaxActiveClusters(&n, gated_cluster_kernel<TILING>, &cfg) != cudaSuccess || n < 1) {
+            cudaOccupancyMaxActiveClusters(&n, gated_cluster_kernel<TILING>, &cfg) != cudaSuccess) {
             cudaGetLastError();
-            n = 1;
+            n = 0;
         }
-        known[split].store(n);
-    }
-    return n;
+        return n;
+    });
 }
 
 template <int TILING>
@@ -586,17 +586,21 @@ struct Plan {
 constexpr int PERSISTENT = -1;
 
 template <int TILING>
-void consider(int64_t tiles, int64_t num_kb, double block_us, double fixed_us, double split_us, Plan &best,
+bool consider(int dev, int64_t tiles, int64_t num_kb, double block_us, double fixed_us, double split_us, Plan &best,
               double &best_us)
 {
     for (int split = 1; split <= MAX_SPLIT && split <= num_kb; ++split) {
-        const int64_t at_once = clusters_at_once<TILING>(split), waves = (tiles + at_once - 1) / at_once;
+        const int64_t at_once = clusters_at_once<TILING>(dev, split);
+        if (at_once == 0)
+            return false;
+        const int64_t waves = (tiles + at_once - 1) / at_once;
         const double us = waves * ((num_kb + split - 1) / split * block_us + fixed_us + (split - 1) * split_us);
         if (us < best_us) {
             best_us = us;
             best = {TILING, split};
         }
     }
+    return true;
 }
 
 // The shortest estimate: waves x (contraction blocks of a CTA x time per block
@@ -607,20 +611,26 @@ void consider(int64_t tiles, int64_t num_kb, double block_us, double fixed_us, d
 // against every other tiling and split for 1 to 1500 tokens and widths of 128
 // to 18432, the choice was the fastest or within 5 % of it: 333 tokens through
 // 7168 x 2048 take 18.7 us split in two against 29.1 us in persistent tiles,
-// through 2048 x 8192 29.0 against 22.8.
-Plan choose(int64_t M, int64_t I, int64_t K)
+// through 2048 x 8192 29.0 against 22.8. The choice fixes the order of the sums,
+// so it goes by the shape and the device alone: false (no plan) when the device
+// does not say how many clusters it runs.
+bool choose(int64_t M, int64_t I, int64_t K, Plan &best)
 {
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
     const int64_t sms = sm_count() > 0 ? sm_count() : 1, num_kb = K / BK, cols = I / BI, rows = (M + 127) / 128;
-    Plan best = {PERSISTENT, 1};
+    best = {PERSISTENT, 1};
     double best_us = (double)((rows * cols + sms - 1) / sms) * (num_kb * 0.43 + 5.0);
     if (M <= Shape<FEW>::TOK) {
         // (always: wide weights are bound by the memory, which the estimates
         // leave out; one token through 7168 x 18432: 43 us, persistent 58)
         best_us = 1e30;
-        consider<FEW>(cols, num_kb, 0.45, 4.1, 0.15, best, best_us);
-    } else if (rows * cols <= sms)
-        consider<ROWS>(rows * cols, num_kb, 0.38, 7.6, 0.35, best, best_us);
-    return best;
+        return consider<FEW>(dev, cols, num_kb, 0.45, 4.1, 0.15, best, best_us);
+    }
+    return rows * cols > sms || consider<ROWS>(dev, rows * cols, num_kb, 0.38, 7.6, 0.35, best, best_us);
 }
 
 }  // namespace
@@ -657,7 +667,9 @@ extern "C" int fp8_gated_gemm(const uint8_t *xq, const float *sx, int64_t ldx, i
     g.gu = static_cast<uint16_t *>(gu), g.ld_gu = ldgu;
     g.pow2 = pow2;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const Plan plan = choose(M, I, K);
+    Plan plan;
+    if (!choose(M, I, K, plan))
+        return FP8FG_ECUDA;
     switch (plan.tiling) {
     case FEW: return launch_clusters<FEW>(g, plan.split, s);
     case ROWS: return launch_clusters<ROWS>(g, plan.split, s);
