@@ -597,8 +597,8 @@ FP8FG_API int fp8fg_device_status(void *stream);
 FP8FG_API int fp8fg_version(void);
 
 /* Test hook: when `skip` != 0, the next fp8_gemm_blockscaled, fp8_gemm_mx,
- * fp8_grouped_gemm_mx, fp8_quant_1x128_dual(_pow2), fp8_gated_gemm or
- * fp8_gated_bwd launch on the current
+ * fp8_grouped_gemm_mx, fp8_quant_1x128_dual(_pow2), fp8_rmsnorm,
+ * fp8_rmsnorm_bwd, fp8_gated_gemm or fp8_gated_bwd launch on the current
  * device withholds its first operand load (a fp8_grouped_gemm launch
  * clears the request without using it), so the consumers' bounded waits
  * run out and the launch reports FP8FG_ETIMEOUT. One-shot; returns
