@@ -5,13 +5,16 @@ Each translation unit compiles in parallel; the CUDA objects link into one
 shared library with the CUDA runtime linked statically, so the library loads
 on a machine without a GPU driver (nothing runs until a call is made). The
 helper reads the metadata of torch tensors and is compiled against the
-installed torch.
+installed torch; it is made anew for another torch or Python. Only the operators
+between a gated MLP's GEMMs need it, so where it cannot be made (no headers)
+build() says so and leaves the library.
 """
 import importlib.util
 import os
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -43,7 +46,10 @@ def _deps():
 
 
 def helper_command(out):
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch is not installed")
+    torch = spec.submodule_search_locations[0]
     inc, lib = os.path.join(torch, "include"), os.path.join(torch, "lib")
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-I", INCLUDE,
             "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem",
@@ -51,23 +57,51 @@ def helper_command(out):
             "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10"]
 
 
+def _made_for():
+    """What the helper depends on beside its sources: the compiler's command,
+    Python's ABI and torch's version (read from its file: importing it is slow)."""
+    command = helper_command("")
+    version = os.path.join(importlib.util.find_spec("torch").submodule_search_locations[0], "version.py")
+    with open(version) as f:
+        return "\n".join(command + [str(sysconfig.get_config_var("SOABI")), f.read()])
+
+
 def build_helper(force=False):
+    made_for, stamp = _made_for(), os.path.join(BUILD, "tensors.made_for")
     newest = max(os.path.getmtime(f) for f in (HELPER_SOURCE, os.path.join(INCLUDE, "fp8fg.h")))
-    if not force and os.path.exists(HELPER) and os.path.getmtime(HELPER) >= newest:
-        return HELPER
+    if not force and os.path.exists(HELPER) and os.path.getmtime(HELPER) >= newest and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read() == made_for:
+                return HELPER
     tmp = HELPER + ".tmp.%d" % os.getpid()
-    r = subprocess.run(helper_command(tmp), capture_output=True, text=True)
+    try:
+        r = subprocess.run(helper_command(tmp), capture_output=True, text=True)
+    except OSError as e:
+        raise RuntimeError("%s: no host compiler (%s)" % (HELPER_SOURCE, e))
     if r.returncode != 0:
         raise RuntimeError("%s failed:\n%s\n%s" % (HELPER_SOURCE, r.stdout, r.stderr))
+    # (the record goes first and comes back last: a build cut short in between is made again)
+    if os.path.exists(stamp):
+        os.remove(stamp)
     os.replace(tmp, HELPER)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(stamp, "w") as f:
+        f.write(made_for)
     return HELPER
 
 
-def build(force=False, verbose=False, extra=()):
+def build(force=False, verbose=False, extra=(), strict=False):
+    """The library, and the helper beside it. A helper that cannot be made is a
+    warning (an error with `strict`)."""
     with ThreadPoolExecutor(max_workers=1) as ex:
         helper = ex.submit(build_helper, force)
         lib = build_lib(force, verbose, extra)
-        helper.result()
+        try:
+            helper.result()
+        except RuntimeError as e:
+            if strict:
+                raise
+            warnings.warn("the operators between a gated MLP's GEMMs are not available: %s" % e, RuntimeWarning)
     return lib
 
 
