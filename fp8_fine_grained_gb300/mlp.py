@@ -43,8 +43,11 @@ def quantize(gamma, w13, w2, eps=1e-6):
 def forward(x, residual, w, save=False):
     """x bf16 [T, D] and residual (the same, or None). Returns (y bf16 [T, D],
     h bf16 [T, D], Saved or None): h is the residual stream for the next
-    block, Saved what backward needs (save=True)."""
+    block, Saved what backward needs (save=True, T % 128 == 0)."""
     import fp8_fine_grained_gb300 as fg
+    if save and x.shape[0] % 128:
+        raise ValueError("save=True is for the backward pass, which takes tokens in multiples of 128; got %d"
+                         % x.shape[0])
     nq, ns, h, rstd = fg.fp8_rmsnorm(x, w.gamma, w.eps, residual=residual)
     aq, sa, gu = fg.fp8_gated_gemm(nq, ns, w.w13, w.s13, save=save)
     y = fg.fprop(aq, sa, w.w2, w.s2)
