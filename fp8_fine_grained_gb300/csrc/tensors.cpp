@@ -127,7 +127,8 @@ bool typed_tensor(PyObject *const *args, Py_ssize_t nargs, Py_ssize_t want)
 }
 
 // matrix(t, dtype, rows, cols, name) -> row pitch of a 2-D row-major tensor of
-// the dtype that covers [rows, cols]
+// the dtype that covers [rows, cols]; for a tensor of one row, whose stride
+// means nothing, one that every entry point takes
 PyObject *matrix(PyObject *, PyObject *const *args, Py_ssize_t nargs)
 {
     return guarded([&]() -> PyObject * {
@@ -142,7 +143,8 @@ PyObject *matrix(PyObject *, PyObject *const *args, Py_ssize_t nargs)
         if (t.size(0) < rows || t.size(1) < cols)
             return PyErr_Format(PyExc_ValueError, "%U must cover [%lld, %lld], got (%lld, %lld)", args[4], rows, cols,
                                 (long long)t.size(0), (long long)t.size(1));
-        return PyLong_FromLongLong(t.stride(0));
+        // (one row has no pitch: torch lets its stride be anything)
+        return PyLong_FromLongLong(t.size(0) == 1 ? (t.size(1) + 15) / 16 * 16 : t.stride(0));
     });
 }
 
