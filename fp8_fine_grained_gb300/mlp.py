@@ -25,6 +25,8 @@ the tokens by 128.
 """
 from collections import namedtuple
 
+import torch
+
 Weights = namedtuple("Weights", "gamma w13 s13 w2 s2 eps")
 Saved = namedtuple("Saved", "h rstd gu")
 Grads = namedtuple("Grads", "dx dw13 dw2 dgamma")
@@ -60,6 +62,9 @@ def backward(dy, saved, w, dres=None):
     and of the residual alike) and the FP32 gradients dw13 [2I, D], dw2 [D, I]
     and dgamma [D]."""
     import fp8_fine_grained_gb300 as fg
+    if dy.shape[0] == 0:  # sums over no tokens (the GEMMs take no empty contraction)
+        zeros = [torch.zeros(s, device=dy.device) for s in (w.w13.shape, w.w2.shape, w.gamma.shape)]
+        return Grads(torch.empty_like(dy), *zeros)
     dyq, sdy, dyqT, sdyT = fg.fp8_quant_1x128_dual(dy)
     da = fg.dgrad(dyq, sdy, w.w2, w.s2)
     dq, ds, dqT, dsT, aqT, saT = fg.fp8_gated_bwd(saved.gu, da)
