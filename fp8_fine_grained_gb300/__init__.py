@@ -806,7 +806,8 @@ def grad_clip(grads, max_norm, eps=1e-6, out=None, norm=None, stream=None):
 
     grads: contiguous float32 or bfloat16 CUDA tensors of any shape (views into
     a bucket included). out: tensors to write, of the same sizes and types
-    (default: the gradients themselves). Returns (norm, out): norm float32 [2]
+    (default: the gradients themselves). No two tensors overlap, except that an
+    output may be its own gradient. Returns (norm, out): norm float32 [2]
     on the device holds the norm before scaling and the factor min(1, max_norm
     / (norm + eps)); nothing is copied to the host."""
     if stream is not None:

@@ -16,15 +16,15 @@ struct Sigmoid2 {
 // and sums are (8 2^-24 relative, however large |v| is).
 //
 // A rounded exponent of 2^(-v log2 e) alone would make e wrong by |v| 2^-24.
-// So the exponent h is -v log2 e rounded to a multiple of 2^-12, which FP32
-// holds with room to spare, and what the rounding left out, lo = -v - h ln 2 in
-// two fused steps, comes back as the factor 1 + lo (lo below 2^-13; the next
-// term of exp(lo) below 2^-27). e and 1 are carried with a factor 2^-64, so that
-// neither e nor the quotient leaves the range of normal numbers from v = -110,
-// where sigmoid(v) rounds to 0, up to v = 43, where c no longer counts beside s;
-// c is 0 beyond. The result's factor 2^-64 is exact, or one rounding to a
-// subnormal number. The hardware's power of two is good to 2 ulp, its reciprocal
-// to 1.
+// So the argument is split in Cody and Waite's manner: the exponent h is -v log2 e
+// rounded to a multiple of 2^-12, which FP32 holds with room to spare, and what
+// the rounding left out, lo = -v - h ln 2 in two fused steps, comes back as the
+// factor 1 + lo (lo below 2^-13; the next term of exp(lo) below 2^-27). e and 1
+// are carried with a factor 2^-64, so that neither e nor the quotient leaves the
+// range of normal numbers from v = -110, where sigmoid(v) rounds to 0, up to v =
+// 43, where c no longer counts beside s; c is 0 beyond. The result's factor 2^-64
+// is exact, or one rounding to a subnormal number. The hardware's power of two is
+// good to 2 ulp, its reciprocal to 1.
 //
 // The bare approximations (a rounded exponent, flushed to zero below 2^-126) are
 // six instructions a pair, this is thirteen: the gate backward of 4096 x 18432

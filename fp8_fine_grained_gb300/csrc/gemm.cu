@@ -572,9 +572,11 @@ __device__ __forceinline__ void skinny_roles(const CUtensorMap *tmX, const CUten
 // ahead of its partner at most, so two sets of maxima suffice. All stores pass
 // through the warp's staging block as in the other epilogues (whole 32-byte
 // sectors straight from the registers were within 1 %). Returns false when the
-// (bounded) wait for the partner ran out. The gate and the exchange cost
-// nothing measurable: 4096 x 7168 x 18432 takes 839 us, 867 with gu, and the
-// plain product of the same size 870 (2.16 TFLOP, 2.5 PFLOP/s).
+// (bounded) wait for the partner ran out. The exchange costs nothing measurable,
+// the gate about 1 % (gate.cuh). 4096 x 7168 x 18432 in bursts of 5 calls, and in
+// 200 in a row, which run at the power cap's clocks: 808 and 845 us, with gu 861
+// and 895, the plain product of the same size 815 and 850 (2.16 TFLOP, 2.4 to 2.7
+// PFLOP/s).
 template <class L>
 __device__ __forceinline__ bool gated_epilogue(const Params &p, uint8_t *smem, float2 (&acc)[64], int64_t row,
                                                bool row_ok, const Tile &tl, int64_t col0, int ew, int lane,
@@ -835,8 +837,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                 tma_load_2d(b_dst + B_STAGE_BYTES / 2, &tmB, (int32_t)tl.n0 + 128, kb * BK, fb);
                         } else if constexpr (MODE == GATED) {
                             // 64 rows x {gate, up} x 2 runs in one copy (four
-                            // boxes of 64 rows: 898 us instead of 839 for 4096
-                            // x 7168 x 18432 without gu)
+                            // boxes of 64 rows took 7 % longer: 898 us and 839
+                            // in one run, 4096 x 7168 x 18432 without gu)
                             tma_load_4d(b_dst, &tmB, kb * BK, 0, 0, (int32_t)(tl.n0 / GATED_RUN), fb);
                         } else {
                             tma_load_2d(b_dst, &tmB, kb * BK, (int32_t)tl.n0, fb);

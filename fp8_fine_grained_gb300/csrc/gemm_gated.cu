@@ -16,8 +16,8 @@
 // is a stream of the weights, which one SM cannot draw at more than about 80
 // GB/s: only the split gives a narrow weight (2048 columns are 16 tiles) enough
 // CTAs. One token through 7168 x 18432 (144 tiles, no split) takes 43 us, 0.90
-// of the copy bandwidth; 24 tokens through 7168 x 2048 take 29.1, 17.0, 11.4
-// and 10.3 us with S = 1, 2, 4 and 6.
+// of the copy bandwidth; 24 tokens through 7168 x 2048 take 29.0, 17.0, 11.5
+// and 10.5 us with S = 1, 2, 4 and 6.
 //
 // The cluster tilings (12 warps):
 //   warp 0      TMA producer: per 128-wide contraction block the 32 KB of
@@ -132,7 +132,7 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank)
 // the gate and the codes. NT tokens of a warp share one division sequence for
 // their scales (lane n on token n); with one per token the divisions are a
 // third of this part's instructions. ROWS, 333 tokens through 7168 x 2048: NT
-// = 8 18.7 us, NT = 1 19.3; FEW has a token or two per warp and takes NT = 1.
+// = 8 19.4 us, NT = 1 19.8; FEW has a token or two per warp and takes NT = 1.
 template <uint32_t PITCH, int NT>
 __device__ __forceinline__ void finish_tokens(const ClusterParams &p, uint32_t sbase, int rank, int warp, int lane,
                                               int nrows, int64_t m0, int64_t i0)
@@ -610,8 +610,8 @@ bool consider(int dev, int64_t tiles, int64_t num_kb, double block_us, double fi
 // (ROWS) and 8.5 / 29.1 (persistent, which has no cluster barriers). Measured
 // against every other tiling and split for 1 to 1500 tokens and widths of 128
 // to 18432, the choice was the fastest or within 5 % of it: 333 tokens through
-// 7168 x 2048 take 18.7 us split in two against 29.1 us in persistent tiles,
-// through 2048 x 8192 29.0 against 22.8. The choice fixes the order of the sums,
+// 7168 x 2048 take 19.4 us split in two against 29.6 us in persistent tiles,
+// through 2048 x 8192 28.7 (no split) against 22.7. The choice fixes the order of the sums,
 // so it goes by the shape and the device alone: false (no plan) when the device
 // does not say how many clusters it runs.
 bool choose(int64_t M, int64_t I, int64_t K, Plan &best)
@@ -626,7 +626,7 @@ bool choose(int64_t M, int64_t I, int64_t K, Plan &best)
     double best_us = (double)((rows * cols + sms - 1) / sms) * (num_kb * 0.43 + 5.0);
     if (M <= Shape<FEW>::TOK) {
         // (always: wide weights are bound by the memory, which the estimates
-        // leave out; one token through 7168 x 18432: 43 us, persistent 58)
+        // leave out; one token through 7168 x 18432: 43 us, persistent 56)
         best_us = 1e30;
         return consider<FEW>(dev, cols, num_kb, 0.45, 4.1, 0.15, best, best_us);
     }

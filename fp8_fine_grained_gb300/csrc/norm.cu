@@ -19,9 +19,11 @@
 // before its first output is known, so a CTA that loads, reduces and stores one
 // row after the other leaves the memory idle most of the time. Each CTA
 // therefore has its next rows brought into a ring in shared memory by bulk
-// copies (about 170 KB in flight per SM, whatever the row's width) while it
-// works on the current one; the row's values stay in registers from there to
-// the last store, so each tensor crosses the memory once.
+// copies while it works on the current one; the row's values stay in registers
+// from there to the last store, so each tensor crosses the memory once. In
+// flight per SM from 1024 columns on: 80 to 190 KB forward and 96 to 216
+// backward (rows of over 8192 columns without a residual 48 to 72 forward);
+// narrower rows are bound by their CTAs' number, 14 KB at 128 columns.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -170,9 +172,10 @@ __device__ __forceinline__ float group_max(const float (&m)[CPT])
 // CTAs placed unevenly, on whichever SMs drain first, so a CTA lets the
 // next kernel start after its last row (on entry when it has one row only:
 // there the next kernel's set-up hides behind this one), and the shared memory
-// asked for leaves no room for a further CTA on the SM. 8192 rows of 7168
-// after another kernel: 36.5 us (without a residual), with an early start and
-// without the padding 42.4; backward of 28672 rows of 2048: 59.3, early 92.
+// asked for leaves no room for a further CTA on the SM. In a stream of such
+// calls, with an early start and without the padding in brackets: forward 8191 x
+// 7168 with a residual 63.6 us (67.7), 8192 x 5120 without 23.9 (33.5). Backward
+// the kernel for dgamma runs in between, and both are alike.
 constexpr int MAX_SLOTS = 3;
 constexpr uint32_t BAR_BYTES = (8 * MAX_SLOTS + 15) / 16 * 16;  // (gamma follows)
 
@@ -243,10 +246,18 @@ struct NormFwd {
 };
 
 // 7 bytes per element with a residual: 8191 x 7168 in 63.4 us, 6.5 TB/s or 0.96
-// of the measured copy, 4096 x 18432 in 85 us (0.91). Without one (3 bytes) it
-// is bound by issue and latency, 110 warp instructions per 256 elements: 8192 x
-// 7168 in 34.5 us, 0.75; with one CTA more per SM (at 64 registers) narrow rows
-// gained nothing and 5120 columns went from 33 us to 35.
+// of the measured copy. Without one (3 bytes) it is bound by issue and latency,
+// 110 warp instructions per 256 elements: 8192 x 7168 in 34.5 us, 0.75; with one
+// CTA more per SM (at 64 registers) narrow rows gained nothing and 5120 columns
+// went from 33 us to 35.
+//
+// The widest rows lose by what the others gain from: 4096 x 18432 with a residual
+// takes 86 us (0.91), and took 80 when each chunk's group was reduced by itself
+// and not the thread's groups together (group_max).
+//
+// The mean is the sum times 1 / D as FP32 rounds it: with the reciprocal root's
+// ulp, rstd is within 3 2^-24 of the sum's root. Over 12000 rows of 7168 rstd's
+// error is 4.2e-8 rms; by torch's mean and 1 / sqrt 4.6e-8.
 //
 // One row per CTA at a time: thread t owns chunks t, t + blockDim, ...; a
 // half-warp's 16 chunks are one 128-column group (D % 128 == 0 and blockDim
@@ -375,8 +386,8 @@ __global__ void __launch_bounds__(max_threads(W), min_ctas(W, false)) rmsnorm_fw
 // rows 16*part .. +15 and each of its threads a pair of columns (a 32-bit word
 // of every row); the parts' maxima meet in shared memory and each thread writes
 // its 2 x 16 codes, which pass through shared memory so that eight threads
-// write whole 128-byte runs of a row of the output. 8192 x 7168: 30.5 us (3.03
-// bytes per element, 0.85 of the measured copy); 39 with 16-byte stores
+// write whole 128-byte runs of a row of the output. 8192 x 7168: 32.9 us (3.03
+// bytes per element, 0.80 of the measured copy); 39 with 16-byte stores
 // straight from the registers, half a sector each.
 constexpr int NT_COLS = 64;
 
@@ -480,9 +491,9 @@ struct NormBwd {
     int skip_first_load;  // test hook: row 0 is never fetched, so that the wait for it runs out
 };
 
-// 8 bytes per element with dres: 8192 x 7168 in 74.5 us with the reduction of
-// dgamma (about 4 us of it), 6.3 TB/s or 0.93 of the measured copy; 6 bytes
-// without: 57.7 us, 0.90.
+// 8 bytes per element with dres: 8192 x 7168 in 74.9 us with the reduction of
+// dgamma (about 4 us of it), 6.3 TB/s or 0.92 of the measured copy; 6 bytes
+// without: 57.9 us, 0.90.
 //
 // The thread's columns are the same in every row, so its dgamma terms add up
 // in registers and leave once, as the CTA's row of `part`.
@@ -490,7 +501,7 @@ struct NormBwd {
 // depend on the schedule. The row's values go from the ring to registers as
 // they are (bf16), so that the slot can be refilled under the second half of
 // the row's work: with two slots a CTA then always has two rows in flight
-// (8192 x 7168 with dres 74.5 us; 87 when the row was read from the ring
+// (8192 x 7168 with dres 74.9 us; 87 when the row was read from the ring
 // twice and held its slot).
 template <int W, bool RES>
 __global__ void __launch_bounds__(max_threads(W), min_ctas(W, true)) rmsnorm_bwd_kernel(const NormBwd p)
@@ -721,9 +732,10 @@ int ring_grid(int64_t T, const RingShape &r)
 }
 
 // The backward pass of few rows takes fewer CTAs than fit, since dgamma's second
-// kernel adds up a row from each: two rows each at least, and four CTAs per SM
-// until every one of a full grid has four (us in a graph, 1031 x 2048 without
-// dres: 912 CTAs 10.0, 608 7.8; 300 x 7168: 300 CTAs 9.4, 152 7.2).
+// kernel adds up a row from each: about two rows each, and four CTAs per SM
+// until every one of a full grid has four (us in a graph, as many CTAs as fit in
+// brackets: 1031 x 2048 without dres 8.5 (10.4), 300 x 7168 with dres 9.1
+// (10.1), 2048 x 512 with dres 7.4 (9.3)).
 int bwd_grid(int64_t T, RingShape r)
 {
     const int64_t sms = sm_count() > 0 ? sm_count() : 1;

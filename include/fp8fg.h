@@ -480,7 +480,8 @@ FP8FG_API int fp8_rmsnorm(const void *x, int64_t ldx, const void *residual, int6
  * layout of fp8_quant_1x128 with transpose = 1 (groups of 128 rows of a
  * column): the activation operand of the weight gradient.
  *   qT      E4M3 [D][ldqT], ldqT >= T; scalesT FP32 [T/128][ld_sT], ld_sT >= D.
- *   T % 128 == 0, D % 128 == 0, D <= 18432. Alignment as fp8_rmsnorm.
+ *   T % 128 == 0, T <= 128 * 65535, D % 128 == 0, D <= 18432. Alignment as
+ *   fp8_rmsnorm.
  * ------------------------------------------------------------------- */
 FP8FG_API int fp8_rmsnorm_t(const void *h, int64_t ldh, const float *rstd, const void *gamma, int gamma_kind,
                             int64_t T, int64_t D, uint8_t *qT, int64_t ldqT, float *scalesT, int64_t ld_sT,
@@ -558,7 +559,8 @@ FP8FG_API int fp8_gated_bwd(const void *gu, int64_t ldgu, const void *dh, int64_
  *           returns. g and out are device pointers aligned to their element
  *           (not more: views into a flat bucket are fine), out == g scales in
  *           place (nothing is written when coef is 1); otherwise the outputs
- *           overlap no input. n == 0 is allowed.
+ *           overlap no input, and no two tensors of the list overlap. n == 0 is
+ *           allowed.
  *   norm    FP32 [2], device: the norm and coef.
  *   workspace  8-byte aligned, at least fp8fg_grad_clip_workspace(count)
  *           bytes on the current device.
@@ -566,7 +568,8 @@ FP8FG_API int fp8_gated_bwd(const void *gu, int64_t ldgu, const void *dh, int64_
  *   (four sums of pairs, up to 130 squares in all), in FP64 beyond; the order is
  *   fixed, so the result does not vary between calls. Elements beyond 1.6e18
  *   in magnitude may give an infinite norm (coef 0), a NaN gives NaN
- *   everywhere; elements below 1e-23 count as zero in the norm.
+ *   everywhere; elements below 1e-19 lose precision in the norm (their squares
+ *   are subnormal) and below 1e-23 count as zero.
  *   max_norm >= 0, eps >= 0.
  * ------------------------------------------------------------------- */
 typedef struct {
