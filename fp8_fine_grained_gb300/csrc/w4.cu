@@ -302,18 +302,23 @@ __device__ __forceinline__ Segment segment_at(const W4Args &a, const Tables &tab
     }
 }
 
-// Wait, each for no longer than the limit, for the stages in flight behind `stage`.
+// Wait for the copies in flight into `ahead` stages of the ring, `stage` (of `parity`)
+// and those behind it: nothing may land in shared memory that the CTA has left. The stage
+// that was given up on is one of them: its wait ends early where another warp's ran out.
+// Every copy was asked for before this began, so that one limit covers them all (a copy
+// that never comes costs it once).
 __device__ __forceinline__ void drain(uint32_t full_at, int stage, uint32_t parity, int ahead, int ring, uint64_t limit_ns)
 {
-    for (int i = 1; i < ahead; ++i) {
+    const uint64_t t0 = global_timer_ns();
+    for (int i = 0; i < ahead; ++i) {
+        while (!mbar_try_wait(full_at + 8 * stage, parity) && global_timer_ns() - t0 < limit_ns)
+            ;
         if (++stage == ring) {
             stage = 0;
             parity ^= 1;
         }
-        const uint64_t t0 = global_timer_ns();
-        while (!mbar_try_wait(full_at + 8 * stage, parity) && global_timer_ns() - t0 < limit_ns)
-            ;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");  // (scales of a stage whose codes never come)
 }
 
 // Columns [c0, c0 + 128 here) of rows [row0, row0 + rows) of x into shared memory, in
