@@ -489,9 +489,8 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_kernel(const RouteArgs
             second = max(max(second, t), min(first, f));
             first = max(first, f);
         }
-        float mine = first ? key_value(first) : -CUDART_INF_F;
-        if (sums && second)
-            mine += key_value(second);
+        const float best = first ? key_value(first) : -CUDART_INF_F, next = sums && second ? key_value(second) : 0.0f;
+        const float mine = best + next;
         int rank = 0;
 #pragma unroll 4
         for (int h = 0; h < a.groups; ++h) {
@@ -501,10 +500,14 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_kernel(const RouteArgs
         const bool keep = g < a.groups && rank < a.top_groups;
         kept = __ballot_sync(ALL, keep);
         if (a.top_groups < a.groups && !by_logit) {
-            // (the least value kept, the largest dropped; 0 for none)
-            const uint32_t value = order_key(mine), least = __reduce_min_sync(ALL, keep ? value : ALL);
-            const uint32_t next = __reduce_max_sync(ALL, g < a.groups && !keep ? value : 0);
-            regroup = least && next && key_value(least) - key_value(next) <= 2.0f * off + 0x1p-21f * fabsf(key_value(least));
+            // (a group's value is off by less than two scores' errors, half a step of each of
+            // its two choices, however small their sum, and half a step of the sum; none
+            // where it is infinite)
+            const float size = fabsf(best) + fabsf(next), err = isinf(size) ? 0.0f : off + 0x1p-22f * size;
+            // the least that a kept group can be worth, the most that a dropped one can; 0 for none
+            const uint32_t least = __reduce_min_sync(ALL, keep ? order_key(mine - err) : ALL);
+            const uint32_t most = __reduce_max_sync(ALL, g < a.groups && !keep ? order_key(mine + err) : 0);
+            regroup = least && most && least <= most;
         }
 #pragma unroll
         for (int i = 0; i < NE; ++i)
