@@ -489,7 +489,10 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_kernel(const RouteArgs
             second = max(max(second, t), min(first, f));
             first = max(first, f);
         }
-        const float best = first ? key_value(first) : -CUDART_INF_F, next = sums && second ? key_value(second) : 0.0f;
+        // (choices enter by a quarter, exactly: two of the largest or lowest numbers have a sum)
+        const float part = by_logit ? 1.0f : 0.25f;
+        const float best = first ? part * key_value(first) : -CUDART_INF_F;
+        const float next = sums && second ? part * key_value(second) : 0.0f;
         const float mine = best + next;
         int rank = 0;
 #pragma unroll 4
@@ -503,7 +506,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_kernel(const RouteArgs
             // (a group's value is off by less than two scores' errors, half a step of each of
             // its two choices, however small their sum, and half a step of the sum; none
             // where it is infinite)
-            const float size = fabsf(best) + fabsf(next), err = isinf(size) ? 0.0f : off + 0x1p-22f * size;
+            const float size = fabsf(best) + fabsf(next), err = isinf(size) ? 0.0f : 0.25f * off + 0x1p-22f * size;
             // the least that a kept group can be worth, the most that a dropped one can; 0 for none
             const uint32_t least = __reduce_min_sync(ALL, keep ? order_key(mine - err) : ALL);
             const uint32_t most = __reduce_max_sync(ALL, g < a.groups && !keep ? order_key(mine + err) : 0);

@@ -29,3 +29,27 @@ def test_large_biases_of_both_signs(size, score, group_top):
     bias = torch.full((8, 8), -2 * size, device="cuda")
     bias[:, 3], bias[:, 5] = size, -size
     check_route(logits, bias.view(-1), 4, score=score, groups=8, top_groups=4, group_top=group_top)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("group_top", [1, 2])
+def test_lowest_and_largest_biases(score, group_top):
+    """A group of experts with the lowest finite bias is worth more than one with none left, whatever its index;
+    sums of two such biases are compared, not lost."""
+    kw = dict(score=score, groups=4, group_top=group_top)
+    lowest = torch.finfo(torch.float32).min
+    logits = rnd(31, 5, 8)
+    masked = logits.clone()
+    masked[:, [0, 1, 4, 5, 6, 7]] = float("-inf")
+    for top_groups in (1, 2, 3):
+        ids, _ = check_route(masked, torch.full((8,), lowest, device="cuda"), 2, top_groups=top_groups, **kw)
+        assert (ids >= 2).all() and (ids < 4).all()
+        for bias in ([lowest] * 8, [-lowest] * 8, [lowest, lowest, lowest, 0, 0, 0, 1, 1],
+                     [lowest, -lowest, 0, 0, -lowest, lowest, -lowest, -lowest], [lowest / 2] * 4 + [lowest] * 4):
+            bias = torch.tensor(bias, device="cuda")
+            check_route(logits, bias, 2, top_groups=top_groups, **kw)
+            check_route(masked, bias, 2, top_groups=top_groups, **kw)
+    bias = torch.full((64,), lowest, device="cuda")
+    bias[5::9] = 0.25
+    for top_groups in (2, 5):
+        check_route(rnd(32, 40, 64), bias, 6, score=score, groups=8, top_groups=top_groups, group_top=group_top)
