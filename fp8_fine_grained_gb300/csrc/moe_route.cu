@@ -4,11 +4,14 @@
 // score s of an expert is the sigmoid or the softmax of its logit; a bias enters
 // the choice (s + b), not the weight; the experts stand in groups, of which the
 // best are kept (a group's value is the sum of its one or two best choices).
-// The choice is that of the scores as real numbers, equal ones by the lower
-// index:
+// Equal experts and groups go by the lower index:
 //   - Without a bias the logits order the experts as their scores do, so they
-//     are compared themselves.
-//   - Otherwise the choices are computed in FP32 with a known error, and a row in
+//     are compared themselves: the order is that of real numbers. Sums of a group's
+//     two best scores are computed in FP32 with a known error, and compared once more
+//     by their logarithms in FP64 (that of 2 less the sum, where the sum is above 1)
+//     in rows where a kept group and a dropped one are closer than that: scores may
+//     underflow or come close to 1.
+//   - With a bias the choices are computed in FP32 with a known error, and a row in
 //     which two neighbours of the order (the chosen experts and the next one, or
 //     the last kept group and the first dropped) are closer than that error is
 //     decided once more in FP64, for the experts near the border alone (one to a
@@ -401,6 +404,42 @@ __device__ __noinline__ int choose_near(const RouteArgs &a, const L *row, const 
     return lane < a.k && lane < count ? list[lane] : -1;
 }
 
+// log(sigmoid(v)), and log(sigmoid(v) + sigmoid(w)) of v >= w.
+__device__ __forceinline__ double log_sigmoid(double v) { return fmin(v, 0.0) - log1p(exp(-fabs(v))); }
+
+__device__ __forceinline__ double log_of_sum(double v, double w)
+{
+    const double p = log_sigmoid(v);
+    return p > -CUDART_INF ? p + log1p(exp(log_sigmoid(w) - p)) : p;
+}
+
+// What the sum of the scores of a group's two best logits (keys, 0 for none) is compared
+// by, as a real number: scores that underflow or come close to 1 count too. First the
+// sum's logarithm as an integer, then, where that is the same, the logits: of two that
+// FP64 cannot add up the larger one is in front.
+struct SumOrder {
+    long long value;
+    unsigned long long logits;
+};
+
+__device__ __noinline__ SumOrder sum_order(int score, uint32_t first, uint32_t second, float row_max)
+{
+    if (!first)
+        return {order_key(-CUDART_INF), 0};
+    const double v = (double)key_value(first), w = second ? (double)key_value(second) : -CUDART_INF;
+    const unsigned long long logits = (unsigned long long)first << 32 | second;
+    if (score == FP8FG_SOFTMAX) {
+        if (row_max == CUDART_INF_F)  // (infinite logits share the row; the others' scores are 0)
+            return {order_key((double)((v == CUDART_INF) + (w == CUDART_INF))), 0};
+        return {order_key(v - (double)row_max + log1p(exp(w - v))), logits};
+    }
+    if (v == -w)
+        return {order_key(0.0), 0};  // the sum is 1
+    const double sum = log_of_sum(v, w);
+    // (above 1: by the complements' sum, 2 less the scores')
+    return {order_key(sum > 0 ? -log_of_sum(-w, -v) : sum), logits};
+}
+
 template <typename L, int NE>
 __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_kernel(const RouteArgs a)
 {
@@ -429,8 +468,8 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_kernel(const RouteArgs
 
     // what the experts are compared by: the logits, or the choices
     const bool sums = a.groups > 1 && a.group_top == 2;
-    const bool by_logit = !a.bias && !sums;
-    const bool need_sum = a.score == FP8FG_SOFTMAX && (!by_logit || !a.renorm);
+    const bool by_logit = !a.bias;
+    const bool need_sum = a.score == FP8FG_SOFTMAX && (!by_logit || sums || !a.renorm);
     float row_max = 0.0f, row_sum = 1.0f;
     uint32_t key[NE];
     float e_of[NE];
@@ -451,7 +490,10 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_kernel(const RouteArgs
     // (the error of a choice: below 2^-21 for a sigmoid, below 2^-18 of the
     // largest score for a softmax, whose sum adds up to 1024 terms; and half a
     // step of the sum with the bias. Two of them may be off in opposite ways.)
-    const float off = by_logit ? -1.0f : a.score == FP8FG_SOFTMAX ? 0x1p-17f / row_sum : 0x1p-20f;
+    const float off = a.score == FP8FG_SOFTMAX ? 0x1p-17f / row_sum : 0x1p-20f;
+    const auto rough_score = [&](float v) {
+        return a.score == FP8FG_SOFTMAX ? __fdividef(exp_below(v, row_max), row_sum) : rough_sigmoid(v);
+    };
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
         const int e = 32 * i + lane;
@@ -489,10 +531,14 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_kernel(const RouteArgs
             second = max(max(second, t), min(first, f));
             first = max(first, f);
         }
-        // (choices enter by a quarter, exactly: two of the largest or lowest numbers have a sum)
-        const float part = by_logit ? 1.0f : 0.25f;
-        const float best = first ? part * key_value(first) : -CUDART_INF_F;
-        const float next = sums && second ? part * key_value(second) : 0.0f;
+        float best = first ? key_value(first) : -CUDART_INF_F, next = sums && second ? key_value(second) : 0.0f;
+        if (by_logit && sums) {
+            best = first ? rough_score(best) : best;
+            next = second ? rough_score(next) : 0.0f;
+        } else if (!by_logit) {  // (by a quarter, exactly: two of the largest or lowest numbers have a sum)
+            best *= 0.25f;
+            next *= 0.25f;
+        }
         const float mine = best + next;
         int rank = 0;
 #pragma unroll 4
@@ -502,20 +548,36 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_kernel(const RouteArgs
         }
         const bool keep = g < a.groups && rank < a.top_groups;
         kept = __ballot_sync(ALL, keep);
-        if (a.top_groups < a.groups && !by_logit) {
+        if (a.top_groups < a.groups && (sums || !by_logit)) {
             // (a group's value is off by less than two scores' errors, half a step of each of
             // its two choices, however small their sum, and half a step of the sum; none
             // where it is infinite)
-            const float size = fabsf(best) + fabsf(next), err = isinf(size) ? 0.0f : 0.25f * off + 0x1p-22f * size;
+            const float size = fabsf(best) + fabsf(next);
+            const float err = isinf(size) ? 0.0f : (by_logit ? off : 0.25f * off) + 0x1p-22f * size;
             // the least that a kept group can be worth, the most that a dropped one can; 0 for none
             const uint32_t least = __reduce_min_sync(ALL, keep ? order_key(mine - err) : ALL);
             const uint32_t most = __reduce_max_sync(ALL, g < a.groups && !keep ? order_key(mine + err) : 0);
             regroup = least && most && least <= most;
         }
+        if (by_logit && regroup) {
+            regroup = false;
+            const SumOrder sum = sum_order(a.score, first, second, row_max);
+            rank = 0;
+            for (int h = 0; h < a.groups; ++h) {
+                const long long v = __shfl_sync(ALL, sum.value, h << a.log_lanes);
+                const unsigned long long w = __shfl_sync(ALL, sum.logits, h << a.log_lanes);
+                rank += v > sum.value || (v == sum.value && (w > sum.logits || (w == sum.logits && h < g)));
+            }
+            kept = __ballot_sync(ALL, g < a.groups && rank < a.top_groups);
+        }
+        // (beside an infinite logit the others' scores are equal)
+        const bool zeros = by_logit && sums && a.score == FP8FG_SOFTMAX && row_max == CUDART_INF_F;
 #pragma unroll
         for (int i = 0; i < NE; ++i)
             if (32 * i + lane < a.E && !(kept >> (group_of(a, 32 * i + lane) << a.log_lanes) & 1u))
                 key[i] = 0;
+            else if (zeros && key[i] && key[i] != order_key(CUDART_INF_F))
+                key[i] = order_key(0.0f);
     }
 
     // The chosen experts, and one more where the order can be in doubt. The last of

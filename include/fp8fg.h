@@ -608,9 +608,13 @@ FP8FG_API int fp8fg_grad_clip(const fp8fg_grad *grads, int64_t count, float max_
  *   choice, largest first. Equal ones (groups too): the lower index first.
  *   gates[t][j] = scale * s_j, or scale * s_j / (sum of the chosen s) with
  *   renorm = 1. The bias enters the choice alone.
- *   Scores are compared as real numbers (evaluated in FP64 where FP32 cannot
- *   tell two of them apart), so that the choice does not depend on their
- *   rounding.
+ *   Without a bias the logits order the experts, and a group's sum of two scores
+ *   is compared as a real number, so that scores which FP32 or FP64 rounds to 0
+ *   or 1 still differ; beside a logit of +inf the other scores of a softmax are 0
+ *   and in groups with group_top = 2 their experts equal. With a bias the choices
+ *   and their sums are those of FP64 arithmetic (evaluated where FP32 cannot tell
+ *   two of them apart): two sigmoids of logits above 37 are equal there, and a
+ *   bias beyond 2^53 leaves nothing of the score.
  *   Masks: an expert whose logit (or choice) is -inf or NaN is never chosen, and
  *   counts nothing in its group. Where fewer than k experts are left, the last
  *   slots have id -1 (unused, as in fp8_moe_combine) and gate 0. A NaN among a
