@@ -8,9 +8,8 @@
 //   - Without a bias the logits order the experts as their scores do, so they
 //     are compared themselves: the order is that of real numbers. Sums of a group's
 //     two best scores are computed in FP32 with a known error, and compared once more
-//     by their logarithms in FP64 (that of 2 less the sum, where the sum is above 1)
-//     in rows where a kept group and a dropped one are closer than that: scores may
-//     underflow or come close to 1.
+//     in FP64 in rows where a kept group and a dropped one are closer than that: by 2
+//     less the sum where it is above 1, by its logarithm where it underflows.
 //   - With a bias the choices are computed in FP32 with a known error, and a row in
 //     which two neighbours of the order (the chosen experts and the next one, or
 //     the last kept group and the first dropped) are closer than that error is
@@ -109,6 +108,21 @@ __device__ __forceinline__ float warp_max(float v)
     for (int d = 16; d; d >>= 1)
         v = fmaxf(v, __shfl_xor_sync(ALL, v, d));
     return v;
+}
+
+// The least and the largest of the lanes' values (no NaN among them).
+__device__ __forceinline__ float warp_least(float v)
+{
+    float r;
+    asm volatile("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ float warp_most(float v)
+{
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
 }
 
 // exp(v - top); 1 for v = top, infinite or not
@@ -414,13 +428,21 @@ __device__ __forceinline__ double log_of_sum(double v, double w)
 }
 
 // What the sum of the scores of a group's two best logits (keys, 0 for none) is compared
-// by, as a real number: scores that underflow or come close to 1 count too. First the
-// sum's logarithm as an integer, then, where that is the same, the logits: of two that
-// FP64 cannot add up the larger one is in front.
+// by, as a real number: scores that underflow or come close to 1 count too. First an
+// integer of the sum's order, then, where that is the same, the logits: of two that FP64
+// cannot add up the larger one is in front.
 struct SumOrder {
     long long value;
     unsigned long long logits;
 };
+
+// An integer of the order of a positive sum, 0 for 1; below 1e-300 that of its logarithm.
+template <typename F>
+__device__ __forceinline__ long long order_of_sum(double sum, F log_of_it)
+{
+    const long long one = order_key(1.0);
+    return sum >= 1e-300 ? order_key(sum) - one : order_key(log_of_it()) - order_key(-690.0) - one;
+}
 
 __device__ __noinline__ SumOrder sum_order(int score, uint32_t first, uint32_t second, float row_max)
 {
@@ -431,13 +453,17 @@ __device__ __noinline__ SumOrder sum_order(int score, uint32_t first, uint32_t s
     if (score == FP8FG_SOFTMAX) {
         if (row_max == CUDART_INF_F)  // (infinite logits share the row; the others' scores are 0)
             return {order_key((double)((v == CUDART_INF) + (w == CUDART_INF))), 0};
-        return {order_key(v - (double)row_max + log1p(exp(w - v))), logits};
+        const double top = (double)row_max;
+        return {order_of_sum(exp(v - top) + exp(w - top), [&] { return v - top + log1p(exp(w - v)); }), logits};
     }
     if (v == -w)
-        return {order_key(0.0), 0};  // the sum is 1
-    const double sum = log_of_sum(v, w);
-    // (above 1: by the complements' sum, 2 less the scores')
-    return {order_key(sum > 0 ? -log_of_sum(-w, -v) : sum), logits};
+        return {0, 0};  // the sum is 1
+    const double ev = exp(-fabs(v)), ew = exp(-fabs(w)), rv = 1 / (1 + ev), rw = 1 / (1 + ew);
+    const double sum = (v > 0 ? rv : ev * rv) + (w > 0 ? rw : ew * rw);
+    if (sum <= 1)
+        return {order_of_sum(sum, [&] { return log_of_sum(v, w); }), logits};
+    // above 1: by 2 less the sum, that of the complements
+    return {-order_of_sum((v > 0 ? ev * rv : rv) + (w > 0 ? ew * rw : rw), [&] { return log_of_sum(-w, -v); }), logits};
 }
 
 template <typename L, int NE>
@@ -550,14 +576,14 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_kernel(const RouteArgs
         kept = __ballot_sync(ALL, keep);
         if (a.top_groups < a.groups && (sums || !by_logit)) {
             // (a group's value is off by less than two scores' errors, half a step of each of
-            // its two choices, however small their sum, and half a step of the sum; none
-            // where it is infinite)
-            const float size = fabsf(best) + fabsf(next);
-            const float err = isinf(size) ? 0.0f : (by_logit ? off : 0.25f * off) + 0x1p-22f * size;
-            // the least that a kept group can be worth, the most that a dropped one can; 0 for none
-            const uint32_t least = __reduce_min_sync(ALL, keep ? order_key(mine - err) : ALL);
-            const uint32_t most = __reduce_max_sync(ALL, g < a.groups && !keep ? order_key(mine + err) : 0);
-            regroup = least && most && least <= most;
+            // its two choices, however small their sum, and half a step of the sum; infinite
+            // ones are exact)
+            const float size = fabsf(best) + fabsf(next), err = fmaf(0x1p-22f, size, by_logit ? off : 0.25f * off);
+            const bool finite = size < CUDART_INF_F;
+            // the least that a kept group can be worth, the most that a dropped one can
+            const float least = warp_least(keep && finite ? mine - err : CUDART_INF_F);
+            const float most = warp_most(g < a.groups && !keep && finite ? mine + err : -CUDART_INF_F);
+            regroup = least <= most;
         }
         if (by_logit && regroup) {
             regroup = false;
@@ -571,13 +597,15 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_kernel(const RouteArgs
             kept = __ballot_sync(ALL, g < a.groups && rank < a.top_groups);
         }
         // (beside an infinite logit the others' scores are equal)
-        const bool zeros = by_logit && sums && a.score == FP8FG_SOFTMAX && row_max == CUDART_INF_F;
+        if (by_logit && sums && a.score == FP8FG_SOFTMAX && row_max == CUDART_INF_F) {
+#pragma unroll
+            for (int i = 0; i < NE; ++i)
+                key[i] = key[i] && key[i] != order_key(CUDART_INF_F) ? order_key(0.0f) : key[i];
+        }
 #pragma unroll
         for (int i = 0; i < NE; ++i)
             if (32 * i + lane < a.E && !(kept >> (group_of(a, 32 * i + lane) << a.log_lanes) & 1u))
                 key[i] = 0;
-            else if (zeros && key[i] && key[i] != order_key(CUDART_INF_F))
-                key[i] = order_key(0.0f);
     }
 
     // The chosen experts, and one more where the order can be in doubt. The last of
