@@ -127,6 +127,16 @@ def _checks():
     return _helper
 
 
+def helper_built():
+    """Whether the compiled helper (and the library) can be used on this machine.
+    build() leaves the helper out where it cannot be made."""
+    try:
+        _checks()
+    except (RuntimeError, OSError):
+        return False
+    return True
+
+
 def status_str(code):
     return lib().fp8fg_status_str(int(code)).decode()
 

@@ -17,7 +17,7 @@ One layer, per rank:
 1. plan_dispatch: every (token t, slot j) becomes one row of the send
    buffer; rows are ordered by expert (so by destination rank too), then by
    token and slot: a stable counting sort of the slots by expert id (moe_plan
-   on the GPU, torch on the CPU).
+   on the GPU, torch on the CPU and where the compiled helper is not built).
    dest[t, j] is the row; send_counts[r, e] the rows for rank r's local
    expert e.
 2. fp8_quant_1x128_scatter quantises every token once and writes its codes
@@ -79,8 +79,9 @@ def plan_dispatch(topk_ids, n_experts, world):
     valid = ids >= 0
     if bool((ids >= n_experts).any()):
         raise ValueError("expert id out of range")
-    if ids.is_cuda and 1 <= topk_ids.shape[1] <= 16 and 1 <= n_experts <= 4096 and ids.numel() < 1 << 31:
-        import fp8_fine_grained_gb300 as fg
+    import fp8_fine_grained_gb300 as fg
+    if (ids.is_cuda and 1 <= topk_ids.shape[1] <= 16 and 1 <= n_experts <= 4096 and ids.numel() < 1 << 31
+            and fg.helper_built()):
         used = torch.where(valid, ids, torch.full_like(ids, -1)).to(torch.int32).reshape(topk_ids.shape)
         with torch.cuda.device(ids.device):
             dest, offsets, _ = fg.moe_plan(used, n_experts)
