@@ -51,14 +51,14 @@ KINDS = [dict(score=s, groups=g, top_groups=t, group_top=p)
 
 
 @pytest.mark.parametrize("kw", KINDS)
-@pytest.mark.parametrize("shift,spread", [(40.0, 1.0), (36.0, 3.0), (70.0, 20.0), (15.0, 0.5), (500.0, 30.0)])
+@pytest.mark.parametrize("shift,spread", [(40.0, 1.0), (36.0, 3.0), (70.0, 20.0), (15.0, 0.5), (500.0, 30.0), (692.0, 6.0)])
 def test_close_to_one(kw, shift, spread):
     check(shift + spread * rnd(41, 20, 16), 3, **kw)
     check((shift + spread * rnd(42, 20, 16)).to(torch.bfloat16), 3, **kw)
 
 
 @pytest.mark.parametrize("kw", KINDS)
-@pytest.mark.parametrize("shift,spread", [(-100.0, 5.0), (-300.0, 100.0), (-1000.0, 60.0)])
+@pytest.mark.parametrize("shift,spread", [(-100.0, 5.0), (-300.0, 100.0), (-1000.0, 60.0), (-692.0, 6.0)])
 def test_close_to_zero(kw, shift, spread):
     check(shift + spread * rnd(43, 12, 16), 3, **kw)
 
