@@ -396,6 +396,7 @@ struct XStage {
                     const uint32_t w = u[q] & 0x7FFF7FFFu;
                     m = __vmaxu2(m, w & ~__vcmpgeu2(w, 0x7F807F80u));
                 }
+                m = __vmaxu2(m, 141u << 7);  // (a factor of 1 at least, which leaves them infinite)
             }
             uint32_t e = max(m & 0xFFFFu, m >> 16);
 #pragma unroll
@@ -697,10 +698,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                                 const float x1 = __uint_as_float(lds32<half * 4>(sx_now[n][1]));
 #pragma unroll
                                 for (int p = 0; p < P; ++p) {
-                                    acc[p][n][0] = fmaf(c[p][n][0] * x0, sw[p][0], acc[p][n][0]);
-                                    acc[p][n][1] = fmaf(c[p][n][1] * x1, sw[p][0], acc[p][n][1]);
-                                    acc[p][n][2] = fmaf(c[p][n][2] * x0, sw[p][1], acc[p][n][2]);
-                                    acc[p][n][3] = fmaf(c[p][n][3] * x1, sw[p][1], acc[p][n][3]);
+                                    // (the two scales first: the sum of the codes' products alone leaves
+                                    // FP32's range where x is large and the weight's scale small)
+                                    acc[p][n][0] = fmaf(c[p][n][0], sw[p][0] * x0, acc[p][n][0]);
+                                    acc[p][n][1] = fmaf(c[p][n][1], sw[p][0] * x1, acc[p][n][1]);
+                                    acc[p][n][2] = fmaf(c[p][n][2], sw[p][1] * x0, acc[p][n][2]);
+                                    acc[p][n][3] = fmaf(c[p][n][3], sw[p][1] * x1, acc[p][n][3]);
                                 }
                             }
                         }

@@ -724,7 +724,10 @@ FP8FG_API int fp8fg_w4_quant(const void *w, int64_t rows, int64_t K, int64_t ldw
  *   the same way and nothing is computed.
  *   x       bf16 [T][ldx]; NaN and infinities carry through to their own row.
  *   wq, sw  codes and scales as fp8fg_w4_quant lays them out, [n_experts][N or
- *           2N][K / 2] and [..][K / group]; any FP32 scales.
+ *           2N][K / 2] and [..][K / group]. Any FP32 scale s with s |x| below
+ *           2^140 for every |x| in 128 columns that have its group among them;
+ *           where s |x| is below 2^-112 for all of them, y may be off by up to
+ *           2^-125 for the group.
  *   y       [n_rows][ldy], FP32 or bf16 per `out`; ldy >= N, any row pitch.
  *   Sums are FP32, in an order that follows from the sizes and the offsets: the
  *   result does not vary between calls. Any number of rows is taken, but every
