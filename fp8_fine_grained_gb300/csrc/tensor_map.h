@@ -48,11 +48,10 @@ inline bool make_map(CUtensorMap *m, const void *base, uint64_t cols, uint64_t r
 
 // Uint8 tensor of rank 3 or 4 over one matrix of row pitch `ld` bytes: `cols`
 // contiguous bytes, then dims[i] steps of strides[i] rows each; box box_cols x
-// box[0] x ..., 128-byte swizzle unless another is given, its rows landing one after the other, the
+// box[0] x ..., 128-byte swizzle, its rows landing one after the other, the
 // first of the further dimensions fastest.
 inline bool make_map_rows(CUtensorMap *m, const void *base, uint64_t cols, uint64_t ld, int n, const uint64_t *dims,
-                          const uint64_t *strides, uint32_t box_cols, const uint32_t *box,
-                          CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B)
+                          const uint64_t *strides, uint32_t box_cols, const uint32_t *box)
 {
     EncodeTiledFn fn = encode_fn();
     if (!fn || n < 1 || n > 3)
@@ -65,7 +64,7 @@ inline bool make_map_rows(CUtensorMap *m, const void *base, uint64_t cols, uint6
         b[i + 1] = box[i];
     }
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)(n + 1), const_cast<void *>(base), d, st, b, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
