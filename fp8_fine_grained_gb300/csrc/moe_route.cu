@@ -26,9 +26,9 @@
 // lane l is 32 i + l. The chosen ones are found without k reductions in turn: the k
 // largest of the lanes' own largest keys give a border, the dozen keys at or above it
 // go to one lane each and are ranked against each other. Bound by the launch and the
-// chain of shuffles (one token, 256 experts in 8 groups: 3.8 us, 2 of them the launch)
-// and by some 1200 instructions a row where there are many (4096 tokens: 10.2 us for
-// 4.5 MB; backward 3.9 us).
+// chain of shuffles (one token, 256 experts in 8 groups: 3.7 us, 2 of them the launch)
+// and by some 1200 instructions a row where there are many (4096 tokens: 10 to 12 us for
+// 4.5 MB, by how many rows FP64 decides; backward 4.0 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math_constants.h>
@@ -444,7 +444,7 @@ __device__ __forceinline__ long long order_of_sum(double sum, F log_of_it)
     return sum >= 1e-300 ? order_key(sum) - one : order_key(log_of_it()) - order_key(-690.0) - one;
 }
 
-__device__ __noinline__ SumOrder sum_order(int score, uint32_t first, uint32_t second, float row_max)
+__device__ __forceinline__ SumOrder sum_order(int score, uint32_t first, uint32_t second, float row_max)
 {
     if (!first)
         return {order_key(-CUDART_INF), 0};
@@ -464,6 +464,21 @@ __device__ __noinline__ SumOrder sum_order(int score, uint32_t first, uint32_t s
         return {order_of_sum(sum, [&] { return log_of_sum(v, w); }), logits};
     // above 1: by 2 less the sum, that of the complements
     return {-order_of_sum((v > 0 ? ev * rv : rv) + (w > 0 ? ew * rw : rw), [&] { return log_of_sum(-w, -v); }), logits};
+}
+
+// The groups to keep by their sums of two scores, lane `g << log_lanes` and those behind
+// it holding the keys of group g's two best logits: bit g << log_lanes of the result.
+__device__ __noinline__ unsigned keep_by_sums(const RouteArgs &a, uint32_t first, uint32_t second, float row_max)
+{
+    const int g = (int)lane_id() >> a.log_lanes;
+    const SumOrder sum = sum_order(a.score, first, second, row_max);
+    int rank = 0;
+    for (int h = 0; h < a.groups; ++h) {
+        const long long v = __shfl_sync(ALL, sum.value, h << a.log_lanes);
+        const unsigned long long w = __shfl_sync(ALL, sum.logits, h << a.log_lanes);
+        rank += v > sum.value || (v == sum.value && (w > sum.logits || (w == sum.logits && h < g)));
+    }
+    return __ballot_sync(ALL, g < a.groups && rank < a.top_groups);
 }
 
 template <typename L, int NE>
@@ -587,14 +602,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_kernel(const RouteArgs
         }
         if (by_logit && regroup) {
             regroup = false;
-            const SumOrder sum = sum_order(a.score, first, second, row_max);
-            rank = 0;
-            for (int h = 0; h < a.groups; ++h) {
-                const long long v = __shfl_sync(ALL, sum.value, h << a.log_lanes);
-                const unsigned long long w = __shfl_sync(ALL, sum.logits, h << a.log_lanes);
-                rank += v > sum.value || (v == sum.value && (w > sum.logits || (w == sum.logits && h < g)));
-            }
-            kept = __ballot_sync(ALL, g < a.groups && rank < a.top_groups);
+            kept = keep_by_sums(a, first, second, row_max);
         }
         // (beside an infinite logit the others' scores are equal)
         if (by_logit && sums && a.score == FP8FG_SOFTMAX && row_max == CUDART_INF_F) {
