@@ -896,7 +896,8 @@ def moe_route(logits, k, bias=None, score="sigmoid", groups=1, top_groups=1, gro
     groups > 1 only the experts of the top_groups groups are taken, whose value
     is the sum of their group_top (1 or 2) best choices. Returns (ids int32
     [T, k], best first, equal ones by index; gates float32 [T, k]): scale times
-    the chosen scores, divided by their sum with renorm. An expert whose logit
+    the chosen scores, divided by their sum with renorm. Scores are compared as
+    real numbers without a bias, with one as FP64 has them. An expert whose logit
     is -inf (or NaN) is never chosen; slots without an expert have id -1 and
     gate 0, which fp8_moe_combine skips. A row with a NaN has NaN gates."""
     if stream is not None:

@@ -13,9 +13,10 @@
 // Arithmetic. A code's value is exact in FP16. x is brought to FP16 exactly:
 // within every 128 columns of a row by a power of two that takes the largest
 // magnitude to [2^14, 2^15). (A bf16 value has 8 significant bits; those below
-// 2^-31 of the block's largest lose some, by at most 2^-40 of it.) The products
-// are exact in FP32, in which the tensor cores add them up within a group; the
-// group's sum times its two scales is added up in FP32 registers.
+// 2^-31 of the block's largest are rounded to FP16's step of 2^-24, by half of it
+// at most: 2^-39 of the largest.) The products are exact in FP32, in which the
+// tensor cores add them up within a group; the group's sum times the product of
+// its two scales is added up in FP32 registers.
 //
 // Shape. A unit is 16 or 32 weight rows (one or two m16n8k16 operands; with the
 // gate, half of them gate rows and half the up rows below them) by up to 8 or 16
@@ -27,11 +28,13 @@
 // not, a cluster of CTAs shares K.
 //
 // Bound by: the stream of the codes where it is long (64 tokens by 8 of 256 experts,
-// 2048 -> 7168: 263 us, 1.74 GB, 0.97 of HBM copy); 5 us of launch, set-up, first
-// loads and join where it is short (one token, 7168 -> 2 x 2048: 7.2 us for 15.6 MB);
-// instructions for integer codes (9 for 8 codes, where E2M1 takes 4: 5 tokens,
-// 18432 -> 7168, groups of 64: 27.0 us for 74.6 MB, of which 5 us stage x and 2 us join
-// the cluster) and for 16 rows (twice the matrix instructions).
+// 2048 -> 7168: 255 to 276 us on different machines, 1.74 GB, 0.93 to 1.0 of HBM copy);
+// 5 us of launch, set-up, first loads and join where it is short (one token, 7168 -> 2 x
+// 2048: 7.1 us for 15.6 MB); instructions for integer codes (9 for 8 codes, where E2M1
+// takes 4: 5 tokens, 18432 -> 7168, groups of 64: 26.5 us for 74.6 MB, of which 5 us stage
+// x and 2 us join the cluster), for 16 rows (twice the matrix instructions: 28672 x 7168 in
+// 44.2 us where 8 rows take 28.4) and, beyond, for every tile of 16 rows anew (91.7 us for
+// 32 rows, 162 for 64).
 // Tried: loads by cp.async with addresses of each lane's own (337 instructions per
 // 32 x 128 codes instead of 234), two CTAs of eight warps per SM with an x each (8
 // experts' gate and up projections of one token 36.8 us instead of 26.3), tiles of 32
@@ -219,6 +222,10 @@ __device__ __forceinline__ void decode(uint32_t w, uint32_t (&h)[4])
             : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
             : "r"(w));
     } else {
+        // The published way to take 4-bit integers apart: a three-input operation masks a
+        // nibble out into the low bits of an FP16 of exponent 1024, and one subtraction (with
+        // a factor of 1/16 for a nibble in the next four bits) leaves its value. Here the
+        // operation also flips the code's sign bit, so that two's complement comes out.
         // (in registers: a three-input operation takes one constant of its own)
         uint32_t low, high, low_base, high_base;
         asm("mov.b32 %0, 0x000F000F;" : "=r"(low));
@@ -810,7 +817,9 @@ struct W4QuantArgs {
 
 // A lane takes 8 columns (16 bytes in, 4 out), G / 8 lanes a group: the group's
 // largest magnitude over the lanes, the scale and its reciprocal by division, one
-// product per value and one rounding to nearest even. A memory stream.
+// product per value and one rounding to nearest even. Once per weight; 32 x 4096 x 7168
+// in groups of 128: 610 us, 2.38 GB, 0.57 of HBM copy (integers 706 us, 0.50), with a 64-bit
+// division and one load in flight a thread and turn.
 template <int KIND, int G>
 __global__ void __launch_bounds__(256) w4_quant_kernel(const W4QuantArgs a)
 {
@@ -1073,7 +1082,11 @@ extern "C" int fp8fg_w4_matvec(const void *x, int64_t ldx, int64_t T, const int3
     // whose rows are few on average, some have more)
     const int64_t share = (n_rows + n_experts - 1) / n_experts;
     const bool small = expert_offsets ? share <= 4 || n_rows <= 8 : n_rows <= 8;
-    // units of 32 rows leave up to one in six SMs idle where there are fewer than six an SM
+    // Units of 32 rows leave up to one in six SMs idle where there are fewer than six an SM,
+    // units of 16 fewer. The limit is higher than it has to be. K = 7168, one row, us with
+    // units of 16 and 32: 2048 weight rows 5.7 and 6.6, 7168 8.9 and 9.4, 8192 9.9 and 9.5,
+    // 12288 14.8 and 11.8, 24320 23.0 and 21.4, 28672 22.9 and 22.1, 58368 42.4 and 36.9. Eight
+    // rows do not fit beside units of 32 there.
     const bool narrow = a.wide * (n_rows < n_experts ? n_rows : n_experts) < 6ll * 32 * sm_count();
     return by_format(kind, group, [&](auto kd, auto g) {
         constexpr int KIND = decltype(kd)::value, G = decltype(g)::value;

@@ -681,7 +681,7 @@ FP8FG_API int fp8fg_moe_plan(const int32_t *ids, int64_t T, int k, int E, int32_
  *   dy      bf16 [y_rows][lddy], overlapping no input. Rows that no slot names
  *           are left as they are; a row that several slots name gets the sum
  *           of their gradients, added up in FP32 in slot order (such rows are
- *           slow: each costs a pass over dest).
+ *           slow: each costs one warp a pass over dest for every 256 columns).
  *   dw      FP32 [T][k]; 0 for slots with a negative dest. A dest >= y_rows is
  *           reported as FP8FG_EDEVICE through fp8fg_device_status and skipped.
  *   workspace  4-byte aligned, at least fp8_moe_combine_bwd_workspace(T, k,
